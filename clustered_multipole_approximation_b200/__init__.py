@@ -12,6 +12,8 @@ Entry points (same names as the C ABI):
     muse_summarize(k, v, assign, C)
     muse_attn_fwd(q, k, v, Cq=..., Ck=..., iters=..., seed=..., topk=..., ...)
     muse_attn_fwd_causal(q, k, v, C=..., block=..., iters=..., seed=..., topk=..., ...)
+    muse_cache_write / muse_cache_read / muse_attn_cache: the paged K/V cache
+    (module kv_cache)
 """
 from __future__ import annotations
 
@@ -66,10 +68,12 @@ EXPORTS = ["muse_workspace_size", "muse_cluster_workspace_size", "muse_cluster",
            "muse_cluster_static_capacity", "muse_device_status", "muse_debug_inject_barrier_fault",
            "muse_attn_bwd_workspace_size", "muse_attn_bwd", "muse_accum_workspace_size",
            "muse_attn_fwd_causal_accum", "muse_attn_bwd_causal_workspace_size",
-           "muse_attn_bwd_causal"]
+           "muse_attn_bwd_causal", "muse_cache_write", "muse_cache_read",
+           "muse_attn_cache_workspace_size", "muse_attn_cache"]
 
 # Bits of the device error word (include/muse.h MUSE_DEVERR_*).
-DEVERR = {1: "MUSE_DEVERR_MMA_WAIT", 2: "MUSE_DEVERR_TEAM_BARRIER", 4: "MUSE_DEVERR_V_RANGE"}
+DEVERR = {1: "MUSE_DEVERR_MMA_WAIT", 2: "MUSE_DEVERR_TEAM_BARRIER", 4: "MUSE_DEVERR_V_RANGE",
+          8: "MUSE_DEVERR_CACHE_INDEX"}
 
 _lib = None
 
@@ -130,6 +134,7 @@ def load_library(path: str = LIB_PATH):
     lib.muse_profile_read.restype = i32
     lib.muse_profile_read.argtypes = [ctypes.c_char_p, i32, ctypes.POINTER(ctypes.c_int),
                                       ctypes.POINTER(ctypes.c_double), i32]
+    kv_cache.declare(lib)
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -487,3 +492,8 @@ def profile_read() -> dict:
         nm = names.raw[i * stride:(i + 1) * stride].split(b"\0", 1)[0].decode()
         out[nm] = (int(launches[i]), float(ms[i]))
     return out
+
+
+from . import kv_cache  # noqa: E402  (it builds on the definitions above)
+from .kv_cache import (attn_cache_workspace_size, make_cache, muse_attn_cache,  # noqa: E402,F401
+                       muse_cache_read, muse_cache_write)

@@ -743,6 +743,7 @@ muse_status muse_device_status(const int32_t* device_error, cudaStream_t stream)
   if (v & MUSE_DEVERR_MMA_WAIT) msg += " a tensor-core completion wait gave up;";
   if (v & MUSE_DEVERR_TEAM_BARRIER) msg += " a k-means team barrier gave up (outputs invalid);";
   if (v & MUSE_DEVERR_V_RANGE) msg += " V holds a finite value outside the fp16 range (output invalid);";
+  if (v & MUSE_DEVERR_CACHE_INDEX) msg += " a length or page-table entry of a cache call is out of range;";
   g_last_error = msg;
   return MUSE_ERR_DEVICE_CHECK;
 }

@@ -71,7 +71,13 @@ enum {
   MUSE_DEVERR_TEAM_BARRIER = 2,
   /* A finite bf16 value of V lies outside the fp16 range (|v| >= 65520), so
    * its fp16 tensor-core operand became infinite; the output is invalid. */
-  MUSE_DEVERR_V_RANGE = 4
+  MUSE_DEVERR_V_RANGE = 4,
+  /* A length or a page-table entry of a paged-cache call lies outside its
+   * range: kv_len not in [0, wide * page_size], new_len not in [0, N], start
+   * < 0, or a needed table entry not in [0, pages).  Lengths are clamped to
+   * their range; a position without a page reads as a zero row and is not
+   * written. */
+  MUSE_DEVERR_CACHE_INDEX = 8
 };
 
 typedef enum { MUSE_BF16 = 0, MUSE_F32 = 1 } muse_dtype;
@@ -354,6 +360,107 @@ muse_status muse_cluster_static(const void *X, muse_dtype dtype, int B, int H,
 
 /* Bytes of the scratch array built into the library for muse_cluster_static. */
 size_t muse_cluster_static_capacity(void);
+
+/*
+ * The paged K/V cache of an attention layer, for answering with a trained
+ * layer: the keys and values of the tokens so far live in fixed-size pages,
+ * new tokens are written as they come, and their queries attend exactly to
+ * everything cached.  (No counterpart on the pages, which train the layer
+ * through; these calls serve it.)
+ *
+ * k and v are [pages, Hkv, page_size, D] in the cache's dtype.  The 8-bit
+ * dtypes carry one fp32 scale per row, k_scale and v_scale [pages, Hkv,
+ * page_size] (else NULL); a stored row stands for its values times its scale:
+ *   MUSE_CACHE_E4M3  scale 2^e, the smallest power of two with max|x| <=
+ *                    448 * 2^e, e >= -126; x / 2^e rounded to e4m3, half to
+ *                    even.
+ *   MUSE_CACHE_I8    scale max|x| / 127 (fp32); 127 x / max|x| rounded to an
+ *                    integer, half to even.
+ *   A row of zeros has scale 1.  A row with an infinity or a NaN is stored as
+ *   zeros with scale NaN, so it stands for a row of NaN.
+ */
+typedef enum {
+  MUSE_CACHE_BF16 = 0,
+  MUSE_CACHE_F32 = 1,
+  MUSE_CACHE_E4M3 = 2,
+  MUSE_CACHE_I8 = 3
+} muse_cache_dtype;
+
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int pages, page_size; /* any page_size >= 1 */
+  muse_cache_dtype dtype;
+} muse_cache;
+
+/* Where a batch of sequences lives in the cache (device pointers).  Position
+ * p of sequence b is row p % page_size of page table[b * wide + p / page_size];
+ * entries of pages that no position below kv_len[b] needs are not read.
+ * kv_len[b] counts the cached tokens of sequence b, the call's new ones
+ * included; new_len[b] (NULL: shape->N for every sequence) says how many of
+ * the call's N token rows sequence b has, and new token i sits at position
+ * kv_len[b] - new_len[b] + i.  wide * page_size <= 2^30. */
+typedef struct {
+  const int32_t *table; /* [B, wide] */
+  const int32_t *kv_len; /* [B] */
+  const int32_t *new_len; /* [B] or NULL */
+  int wide;
+} muse_cache_index;
+
+/* Element strides of a [B, H, N, D] tensor whose last dimension is
+ * contiguous; each must be a multiple of 16 bytes. */
+typedef struct {
+  int64_t b, h, t;
+} muse_strides;
+
+/*
+ * Writes the new tokens' rows of K and V [B,Hkv,N,D] (shape->dtype; strides
+ * ks, vs) into the cache.  Tokens i >= new_len[b] and tokens at negative
+ * positions (new_len[b] > kv_len[b]) are not written.  No two new tokens may
+ * share a cache row (a page named twice where new tokens go): what such a row
+ * holds afterwards is undefined.  shape->Hq is not used.
+ * device_error: one int32 or NULL; set to 0, then to MUSE_DEVERR_* bits.
+ */
+muse_status muse_cache_write(const void *K, const muse_strides *ks, const void *V,
+                             const muse_strides *vs, const muse_shape *shape,
+                             const muse_cache *cache, const muse_cache_index *index,
+                             int32_t *device_error, cudaStream_t stream);
+
+/*
+ * Reads rows back: K and V [B,Hkv,N,D] (contiguous, shape->dtype, the layout
+ * of the whole-sequence operators) receive positions start[b] .. start[b] +
+ * N - 1 of every sequence (start NULL: 0), zero rows at and past kv_len[b].
+ * index->new_len and shape->Hq are not used.
+ */
+muse_status muse_cache_read(void *K, void *V, const muse_shape *shape, const muse_cache *cache,
+                            const muse_cache_index *index, const int32_t *start,
+                            int32_t *device_error, cudaStream_t stream);
+
+/*
+ * Exact attention of the new tokens' queries over the cache: for q-head h and
+ * new token i of sequence b at position P,
+ *   o = sum_t p_t v_t,  p = softmax_t(scale q.k_t),  lse = ln sum_t exp(scale q.k_t)
+ * over the cached positions t <= P (causal != 0; with window > 0 also t >
+ * P - window), or over every t < kv_len[b] (causal == 0: cross attention to
+ * the cached states of another sequence; window must be 0).  One token per
+ * sequence, a chunk of a prompt and a mixed batch are the same call; the new
+ * tokens' own K and V must have been written first.  A row that sees nothing,
+ * or whose logits are all -inf, gives o = 0 and lse = -inf; keys outside a
+ * row's range do not reach it, whatever they hold.  Rows i >= new_len[b] of O
+ * and lse are left as they were.  Q and O [B,Hq,N,D] (strides qs, os; O's rows
+ * must not overlap) share shape->dtype (out_f32 must be 0), lse is [B,Hq,N]
+ * fp32 contiguous or NULL.  Logits and sums are fp32; for bf16 queries the
+ * softmax weights are rounded once to bf16 for the tensor cores (an int8
+ * cache's row scale multiplied in first).  The same call on the same
+ * inputs gives the same bits.
+ */
+size_t muse_attn_cache_workspace_size(const muse_shape *shape, const muse_cache *cache,
+                                      const muse_cache_index *index);
+muse_status muse_attn_cache(const void *Q, const muse_strides *qs, void *O,
+                            const muse_strides *os, float *lse, const muse_shape *shape,
+                            const muse_cache *cache, const muse_cache_index *index, float scale,
+                            int causal, int window, int32_t *device_error, void *ws,
+                            size_t ws_bytes, cudaStream_t stream);
 
 const char *muse_status_string(muse_status status);
 
