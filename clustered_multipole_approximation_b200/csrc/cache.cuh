@@ -171,7 +171,14 @@ struct CacheAttn {
   int causal;
   int window;     // 0: none
   float scale;
-  void* ws;
+  // division of the keys (plan_cache_attn)
+  int RT;         // row tiles of a kv-head
+  int rows;       // packed rows of a tile
+  int S;          // splits a row tile can have
+  int minc;       // keys of a split, at least
+  int PR;         // rows of a split's partial
+  void* ws;       // partial o, then ml
+  float2* ml;
 };
 // Keys that the query at position pos sees: [lo, hi), empty when hi <= lo.
 __device__ inline int2 seen(const CacheAttn& a, const SeqLen& s, int pos) {

@@ -43,7 +43,7 @@ muse_status check_shape(const muse_shape* sh) {
   return MUSE_OK;
 }
 
-muse_status check_cache(const muse_cache* ca, const muse_cache_index* ix) {
+muse_status check_cache(const muse_cache* ca, const muse_cache_index* ix, int Hkv) {
   if (!ca || !ix) return fail(MUSE_ERR_INVALID_ARG, "cache and index must not be NULL");
   if (ca->dtype < MUSE_CACHE_BF16 || ca->dtype > MUSE_CACHE_I8)
     return fail(MUSE_ERR_INVALID_ARG, "unknown cache dtype");
@@ -51,6 +51,8 @@ muse_status check_cache(const muse_cache* ca, const muse_cache_index* ix) {
     return fail(MUSE_ERR_INVALID_ARG, "pages, page_size and wide must be >= 1");
   if ((long long)ix->wide * ca->page_size > 1LL << 30)
     return fail(MUSE_ERR_UNSUPPORTED, "wide * page_size must be <= 2^30");
+  if ((__int128)ca->pages * ca->page_size * Hkv > (1LL << 31) - 1)  // 128 bytes a row of K and V at least
+    return fail(MUSE_ERR_UNSUPPORTED, "pages * Hkv * page_size must be < 2^31");
   if (!ca->k || !ca->v || !ix->table || !ix->kv_len)
     return fail(MUSE_ERR_INVALID_ARG, "k, v, table and kv_len must not be NULL");
   const bool scaled = ca->dtype == MUSE_CACHE_E4M3 || ca->dtype == MUSE_CACHE_I8;
@@ -132,7 +134,7 @@ muse_status muse_cache_write(const void* K, const muse_strides* ks, const void* 
                              const muse_strides* vs, const muse_shape* sh, const muse_cache* ca,
                              const muse_cache_index* ix, int32_t* device_error, cudaStream_t st) {
   muse_status s = check_shape(sh);
-  if (s == MUSE_OK) s = check_cache(ca, ix);
+  if (s == MUSE_OK) s = check_cache(ca, ix, sh->Hkv);
   if (s == MUSE_OK) s = check_strides(ks, sh);
   if (s == MUSE_OK) s = check_strides(vs, sh);
   if (s != MUSE_OK) return s;
@@ -151,7 +153,7 @@ muse_status muse_cache_read(void* K, void* V, const muse_shape* sh, const muse_c
                             const muse_cache_index* ix, const int32_t* start,
                             int32_t* device_error, cudaStream_t st) {
   muse_status s = check_shape(sh);
-  if (s == MUSE_OK) s = check_cache(ca, ix);
+  if (s == MUSE_OK) s = check_cache(ca, ix, sh->Hkv);
   if (s != MUSE_OK) return s;
   if (!K || !V) return fail(MUSE_ERR_INVALID_ARG, "K and V must not be NULL");
   if (misaligned(K, 16) || misaligned(V, 16))
@@ -167,7 +169,7 @@ muse_status muse_cache_read(void* K, void* V, const muse_shape* sh, const muse_c
 
 size_t muse_attn_cache_workspace_size(const muse_shape* sh, const muse_cache* ca,
                                       const muse_cache_index* ix) {
-  if (check_shape(sh) != MUSE_OK || check_cache(ca, ix) != MUSE_OK) return 0;
+  if (check_shape(sh) != MUSE_OK || check_cache(ca, ix, sh->Hkv) != MUSE_OK) return 0;
   return cache_attn_workspace(attn_args(sh, ca, ix, nullptr));
 }
 
@@ -176,7 +178,7 @@ muse_status muse_attn_cache(const void* Q, const muse_strides* qs, void* O, cons
                             const muse_cache_index* ix, float scale, int causal, int window,
                             int32_t* device_error, void* ws, size_t ws_bytes, cudaStream_t st) {
   muse_status s = check_shape(sh);
-  if (s == MUSE_OK) s = check_cache(ca, ix);
+  if (s == MUSE_OK) s = check_cache(ca, ix, sh->Hkv);
   if (s == MUSE_OK) s = check_strides(qs, sh);
   if (s == MUSE_OK) s = check_strides(os, sh);
   if (s != MUSE_OK) return s;

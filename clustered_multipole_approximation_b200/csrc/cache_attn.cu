@@ -1,73 +1,30 @@
-// Attention of a chunk of new tokens over the paged cache.
+// Attention of a chunk of new tokens over the paged cache: the choice of a
+// kernel, the division of the keys, the join of the splits, and the fp32 path.
 //
 // Query i of sequence b, at position P = kv_len - new_len + i, sees the keys
 // [lo, hi) of `seen` and takes
 //   o = sum_t softmax_t(scale q.k_t) v_t,   lse = ln sum_t exp(scale q.k_t);
 // a row that sees nothing has o = 0 and lse = -inf.  One online softmax: the
 // running maximum m and sum l, and o rescaled when m moves.
-#include "cache.cuh"
+#include "cache_attn.cuh"
 #include "kernels.h"
-#include "mma_sync.cuh"
 
 namespace muse {
 
 namespace {
 
-// One warp per query row; lane c of the first D / 8 lanes of each of two (four
-// at D = 64) groups holds columns [8 c, 8 c + 8), a group takes every second
-// (fourth) key.  fp32 throughout.
+// fp32 queries, or an fp32 cache: one warp per query row.
 template <typename T, int CT, int D>
-__global__ void __launch_bounds__(128) cache_attn_simt_kernel(CacheAttn a, long long rows) {
-  constexpr int LPR = D / 8, GR = 32 / LPR;
+__global__ void __launch_bounds__(128) cache_attn_simt_kernel(const __grid_constant__ CacheAttn a,
+                                                              long long rows) {
   const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (r >= rows) return;
-  const int lane = threadIdx.x & 31, col = lane % LPR, grp = lane / LPR;
-  const long long bh = r / a.c.n;
-  const int i = (int)(r - bh * a.c.n);
-  const int b = (int)(bh / a.Hq), hq = (int)(bh - (long long)b * a.Hq);
+  const long long bh = r / (a.c.n * a.G);
+  const int pr = (int)(r - bh * (a.c.n * a.G));
+  const int b = (int)(bh / a.c.Hkv), h = (int)(bh - (long long)b * a.c.Hkv);
   const SeqLen s = seq_len(a.c, b);
-  if (i >= s.nn) return;
-  const int2 ks = seen(a, s, s.pos0 + i);
-  float q[8], o[8] = {}, m = -INFINITY, l = 0.f;
-  load8_in(static_cast<const T*>(a.Q) + b * a.qs.b + hq * a.qs.h + i * a.qs.t + 8 * col, q);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] *= a.scale;
-  for (int t0 = ks.x; t0 < ks.y; t0 += GR) {
-    const int t = t0 + grp;
-    const long long row = t < ks.y ? row_of(a.c, b, hq / a.G, t) : -1;
-    float k[8], v[8], x = 0.f;
-    load8<CT>(a.c.k, a.c.ks, row, D, col, k);
-    load8<CT>(a.c.v, a.c.vs, row, D, col, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x = fmaf(q[e], k[e], x);
-#pragma unroll
-    for (int w = LPR / 2; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-    if (t >= ks.y) continue;
-    const float mn = fmaxf(m, x);
-    // a logit of -inf before any other: nothing is added
-    const float f = m == -INFINITY ? 0.f : expf(m - mn);
-    const float p = x == -INFINITY ? 0.f : expf(x - mn);
-    l = l * f + p;
-    m = mn;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = fmaf(o[e], f, p * v[e]);
-  }
-#pragma unroll
-  for (int w = LPR; w < 32; w <<= 1) {  // join the groups
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, w), l2 = __shfl_xor_sync(0xffffffffu, l, w);
-    const float mn = fmaxf(m, m2);
-    const float f = m == -INFINITY ? 0.f : expf(m - mn), f2 = m2 == -INFINITY ? 0.f : expf(m2 - mn);
-    l = l * f + l2 * f2;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = o[e] * f + __shfl_xor_sync(0xffffffffu, o[e], w) * f2;
-    m = mn;
-  }
-  if (grp) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] *= inv;
-  store8(static_cast<T*>(a.O) + b * a.os.b + hq * a.os.h + i * a.os.t + 8 * col, o);
-  if (a.lse && col == 0) a.lse[r] = l == 0.f ? -INFINITY : m + logf(l);
+  if (pr >= s.nn * a.G) return;
+  redo_row<T, CT, D>(a, s, b, h, pr, 0, s.kv, 0, 0, 1, 0);
 }
 
 template <typename T, int CT>
@@ -80,20 +37,176 @@ void simt_as(const CacheAttn& a, cudaStream_t st) {
     cache_attn_simt_kernel<T, CT, 128><<<blocks, 128, 0, st>>>(a, rows);
 }
 
+// Joins the splits of one row: W warps take every W-th split each, then the
+// CTA's first warp their sums, always in this order.
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(32 * W) cache_join_kernel(const __grid_constant__ CacheAttn a) {
+  constexpr int C = D / 32;  // columns of a lane
+  __shared__ float so[W][D];
+  __shared__ float2 sml[W];
+  const int n = a.c.n, rows = n * a.G;
+  const long long bh = blockIdx.x / rows;
+  const int r = (int)(blockIdx.x - bh * rows);
+  const int b = (int)(bh / a.c.Hkv), h = (int)(bh - (long long)b * a.c.Hkv);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SeqLen s = seq_len(a.c, b);
+  cudaGridDependencySynchronize();
+  if (r >= s.nn * a.G) return;
+  const int rt = r / a.rows;
+  const RowTile t = row_tile(a, s, rt * a.rows, a.rows);
+  const int parts = split_count(a, t.hi - t.lo);
+  if (parts == 1) return;  // the tile wrote its rows itself
+  const long long tile = bh * a.RT + rt;
+  const int pr = r - t.r0;
+  float m = kFloor, l = 0.f, o[C] = {};
+#pragma unroll 4
+  for (int p = warp; p < parts; p += W) {
+    const float2 ml = *part_ml(a, tile, p, pr);
+    const float* po = part_o<D>(a, tile, p, pr) + C * lane;
+    float y[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) y[c] = po[c];
+    // NaN maxima do not arise: they are maxima of the numbers among the logits
+    const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), g = exp2f(ml.x - mn);
+    l = l * f + ml.y * g;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = o[c] * f + y[c] * g;
+    m = mn;
+  }
+  if (W > 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) so[warp][C * lane + c] = o[c];
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp) return;
+    m = kFloor;
+    l = 0.f;
+    for (int w = 0; w < W; ++w) m = fmaxf(m, sml[w].x);
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = exp2f(sml[w].x - m);
+      l += sml[w].y * f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = fmaf(so[w][C * lane + c], f, o[c]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const RowAt at = row_at(a, b, h, r);
+  T* op = static_cast<T*>(a.O) + at.o + C * lane;
+#pragma unroll
+  for (int c = 0; c < C; ++c) st(op + c, o[c] * inv);
+  if (a.lse && lane == 0) a.lse[at.lse] = lse_of(m, l);
+}
+
+template <typename T, int D, int W>
+void join_as(const CacheAttn& a, cudaStream_t st) {
+  // launched while its predecessor drains: it waits for it on the device
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hq * a.c.n));
+  cfg.blockDim = dim3(32 * W);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D, W>, a);
+}
+template <typename T>
+void run_join(const CacheAttn& a, cudaStream_t st) {
+  ProfScope ps(st, "cache_join");
+  if (a.c.D == 64)
+    a.S <= 8 ? join_as<T, 64, 1>(a, st) : join_as<T, 64, 8>(a, st);
+  else
+    a.S <= 8 ? join_as<T, 128, 1>(a, st) : join_as<T, 128, 8>(a, st);
+}
+
+enum Path { kSimt, kStep, kChunk };
+Path path_of(const CacheAttn& a) {
+  if (a.f32 || a.type == kCacheF32) return kSimt;
+  return (long long)a.c.n * a.G <= 16 ? kStep : kChunk;
+}
+
+constexpr int kSMs = 148;
+
+// How the call's keys are divided, from its sizes alone (the lengths are on
+// the device; each row tile then uses the splits that its own length asks
+// for).
+Path plan(CacheAttn& a) {
+  const Path p = path_of(a);
+  a.RT = a.S = a.minc = 1;
+  a.rows = a.PR = 0;
+  if (p == kSimt) return p;
+  const long long cap = (long long)a.c.wide * a.c.page.d;
+  const int size = a.type == kCacheBf16 ? 2 : 1;
+  const long long packed = (long long)a.c.n * a.G;
+  auto quanta = [](long long x) { return (x + kQuantum - 1) / kQuantum * kQuantum; };
+  if (p == kStep) {
+    a.rows = 16;
+    const long long units = (long long)a.B * a.c.Hkv;
+    // keys of a split: enough splits for eight CTAs an SM, none of more than
+    // 256 KB of cache, and no more than 128 a row
+    long long c = quanta(cap * units / (kSMs * 8) + 1);
+    const long long most = quanta((256 << 10) / (2 * a.c.D * size));
+    if (c > most) c = most;
+    if (c * 128 < cap) c = quanta((cap + 127) / 128);
+    a.S = (int)((cap + c - 1) / c);
+    while (a.S > 1 && units * a.S > 0x7FFFFFFF) a.S = (a.S + 1) / 2;  // the grid
+    // a table far wider than its sequences: shorter splits while few rows fill the SMs
+    const long long least = quanta(c * units / (2 * kSMs));
+    a.minc = (int)(least < c ? least : c);
+  } else {
+    a.rows = 256;
+    a.RT = (int)((packed + 255) / 256);
+    const long long units = (long long)a.B * a.c.Hkv * a.RT;
+    // the number of splits whose last wave of CTAs wastes least, each split
+    // charged with 3 % for its partials and start
+    double best = 1e30;
+    for (int S = 1; S <= 64 && (S == 1 || (long long)S * 512 <= cap); ++S) {
+      const double w = (double)((units * S + kSMs - 1) / kSMs) / S * (1 + 0.03 * (S - 1));
+      if (w < best - 1e-9) {
+        best = w;
+        a.S = S;
+      }
+      if (units * S > 8 * kSMs) break;
+    }
+    a.minc = 512;
+  }
+  a.PR = (int)(packed < a.rows ? packed : a.rows);
+  return p;
+}
+
+// Bytes of the split partials: o, then (m, l).
+size_t part_bytes(const CacheAttn& a, bool ml) {
+  const size_t rows = (size_t)a.B * a.c.Hkv * a.RT * a.S * a.PR;
+  return (rows * (ml ? 8 : (size_t)a.c.D * 4) + 255) / 256 * 256;
+}
+
 }  // namespace
 
-size_t cache_attn_workspace(const CacheAttn&) { return 256; }
+size_t cache_attn_workspace(const CacheAttn& a0) {
+  CacheAttn a = a0;
+  plan(a);
+  return a.S > 1 ? part_bytes(a, false) + part_bytes(a, true) : 256;
+}
 
-void run_cache_attn(const CacheAttn& a, cudaStream_t st) {
+void run_cache_attn(const CacheAttn& a0, cudaStream_t st) {
+  CacheAttn a = a0;
+  const Path p = plan(a);
+  if (p != kSimt) {
+    if (a.S > 1) a.ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(a.ws) + part_bytes(a, false));
+    p == kStep ? run_cache_step(a, st) : run_cache_chunk(a, st);
+    if (a.S > 1) run_join<__nv_bfloat16>(a, st);
+    return;
+  }
   ProfScope ps(st, "cache_attn");
   switch (a.type * 2 + a.f32) {
-    case 0: return simt_as<__nv_bfloat16, kCacheBf16>(a, st);
     case 1: return simt_as<float, kCacheBf16>(a, st);
     case 2: return simt_as<__nv_bfloat16, kCacheF32>(a, st);
     case 3: return simt_as<float, kCacheF32>(a, st);
-    case 4: return simt_as<__nv_bfloat16, kCacheE4m3>(a, st);
     case 5: return simt_as<float, kCacheE4m3>(a, st);
-    case 6: return simt_as<__nv_bfloat16, kCacheI8>(a, st);
     default: return simt_as<float, kCacheI8>(a, st);
   }
 }

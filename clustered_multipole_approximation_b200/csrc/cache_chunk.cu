@@ -1,0 +1,594 @@
+// Attention of a chunk of new tokens over the paged cache on the
+// fifth-generation tensor cores (tcgen05, TMEM), bf16 queries.
+//
+// One CTA takes up to 256 packed rows of one (sequence, kv-head) -- all heads
+// that share the keys -- and one split of its keys, in tiles of 128.  Two
+// streams of 128 threads, a thread a row (its TMEM lane), take turns on the
+// tensor cores: while one forms its softmax the other's products run.
+//   S = Q K^T     tcgen05.mma, M = 128 rows, N = 128 keys, both operands in
+//                 shared memory, the accumulator in TMEM;
+//   P             2^(scale log2e S - m) rounded to bf16, stored over S;
+//   O += P V      tcgen05.mma with P from TMEM, V MN-major in shared memory.
+// With more than 128 rows the streams are two halves of the rows over the
+// same key tiles; otherwise they are the even and the odd tiles of the same
+// rows, joined at the end.  m moves only when a logit exceeds it by more than
+// kSlack, so O is rescaled rarely.
+//
+// Pages are gathered by four load warps: a lane looks up the page row of one
+// key, the warp copies whole rows into the 128-byte-swizzled operand form
+// (cp.async; 8-bit rows are converted to bf16, exact, on the way).  Any page
+// size is the same to them.  Scales of 8-bit rows multiply S's and P's
+// columns.
+//
+// Warps 0-7: softmax of stream 0 (0-3) and 1 (4-7); 8-11: loads; 12: products.
+// Every wait is bounded; one that gives up sets kErrMmaWait.
+#include "cache_attn.cuh"
+#include "kernels.h"
+#include "mma_sync.cuh"
+
+namespace muse {
+
+namespace {
+
+constexpr int kKeys = 128;    // keys of a tile
+constexpr int kThreads = 512;
+constexpr int kLoad = 128;    // load threads
+// Registers a thread: 256 softmax x 200 + 128 load x 80 + 128 product x 32
+// = the 512 x 128 of the launch.
+
+__device__ inline int swz(int r, int q) { return r * 128 + ((q ^ (r & 7)) << 4); }
+// K-major operand, 128-byte swizzle, 8-row groups 1 KB apart
+__device__ inline uint64_t desc_k(uint32_t a) {
+  return (uint64_t)((a >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// MN-major operand, 128-byte swizzle: lbo = bytes between 64-element column chunks
+__device__ inline uint64_t desc_mn(uint32_t a, uint32_t lbo) {
+  return (uint64_t)((a >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ inline void umma(uint32_t tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ inline void umma_ts(uint32_t tmem, uint32_t at, uint64_t bd, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem),
+      "r"(at), "l"(bd), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ inline void umma_commit(uint32_t mbar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(mbar)
+               : "memory");
+}
+__device__ inline void mbar_init(uint32_t mbar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(mbar), "r"(count));
+}
+__device__ inline void mbar_arrive(uint32_t mbar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(mbar) : "memory");
+}
+// Bounded wait for the phase of this parity; false when it gave up.
+__device__ inline bool mbar_wait(uint32_t mbar, uint32_t parity) {
+  for (int it = 0; it < (1 << 22); ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+__device__ inline void tld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ inline void tst32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// The wait for this thread's TMEM loads, tied to their registers so that no
+// use of them moves above it.
+__device__ inline void tld_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+                 "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ inline void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ inline void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ inline void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ inline void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ inline void streams_sync() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
+
+template <int CT, int D>
+struct ChunkL {
+  static constexpr int KB = D / 64;           // 64-column chunks
+  static constexpr int QC = 128 * 128;        // bytes of one chunk of 128 rows
+  static constexpr int Q = 0;                 // [stream][chunk][128 rows][128 B]
+  static constexpr int STAGES = Q + 2 * KB * QC;
+  static constexpr int SS = KB * QC;          // one tile of K or V
+  static constexpr int NS = D == 128 ? (CT == kCacheBf16 ? 5 : 4) : 8;
+  static constexpr int LAG = NS == 8 ? 4 : NS - 2;  // copies in flight; load i waits for load i - NS's stage
+  static constexpr int SC = STAGES + NS * SS;  // 8-bit: (k, v) scales [stage][2][128], with V
+  static constexpr int TOTAL = SC + (CT == kCacheBf16 ? 0 : NS * 2 * kKeys * 4) + 1024;
+};
+
+template <int CT, int D>
+__global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_constant__ CacheAttn a) {
+  using L = ChunkL<CT, D>;
+  constexpr bool k8 = CT != kCacheBf16;
+  constexpr int KB = L::KB, NS = L::NS;
+  extern __shared__ __align__(1024) unsigned char chunk_raw[];
+  unsigned char* sm = chunk_raw + ((1024 - (smem_u32(chunk_raw) & 1023)) & 1023);
+  const uint32_t sb = smem_u32(sm);
+  __shared__ __align__(8) uint64_t mFull[NS], mEmpty[NS], mS[2], mP[2], mO[2];
+  __shared__ uint32_t tslot;
+  __shared__ int sbad, sfail;
+  __shared__ float2 jml[128];
+
+  const long long tile = blockIdx.x / a.S;
+  const int split = (int)(blockIdx.x - tile * a.S);
+  const long long bh = tile / a.RT;
+  const int rti = (int)(tile - bh * a.RT);
+  const int b = (int)(bh / a.c.Hkv), h = (int)(bh - (long long)b * a.c.Hkv);
+  const SeqLen s = seq_len(a.c, b);
+  const int r0 = rti * 256;
+  if (r0 >= s.nn * a.G) return;
+  const RowTile rt = row_tile(a, s, r0, 256);
+  const int len = rt.hi - rt.lo, parts = split_count(a, len);
+  if (split >= parts) return;
+  const int keys = split_keys(a, len);
+  const int t0 = rt.lo + split * keys, t1 = min(rt.hi, t0 + keys);
+  const int nt = (max(0, t1 - t0) + kKeys - 1) / kKeys;  // key tiles
+  const bool two = rt.r1 - r0 > 128;  // the streams are row halves (else tile parities)
+  auto steps = [&](int w) { return two ? nt : (nt - w + 1) >> 1; };
+  auto tile_at = [&](int w, int k) { return two ? k : 2 * k + w; };
+  // loads in the order of their use: K0, K1, V0, K2, V1, ... K[nt - 1], V[nt - 2],
+  // V[nt - 1]; the number of a load is its place in that order.  The stage of
+  // load i is freed by products that need no load past i + 1.
+  auto k_item = [](int t) { return t == 0 ? 0 : 2 * t - 1; };
+  auto v_item = [&](int t) { return min(2 * t + 2, 2 * nt - 1); };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tslot)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    if (lane == 0) {
+      for (int i = 0; i < NS; ++i) {
+        mbar_init(smem_u32(&mFull[i]), kLoad / 32);
+        mbar_init(smem_u32(&mEmpty[i]), 1);
+      }
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(smem_u32(&mS[w]), 1);
+        mbar_init(smem_u32(&mP[w]), 4);
+        mbar_init(smem_u32(&mO[w]), 1);
+      }
+      sbad = sfail = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;\n");
+    }
+  }
+  {  // the query rows; rows past the tile are zero
+    const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
+    constexpr int P = D / 8;  // 16-byte pieces of a row
+    for (int e = tid; e < (two ? 256 : 128) * P; e += kThreads) {
+      const int r = e / P, q = e % P;
+      const bool live = r0 + r < rt.r1;
+      const long long src = live ? row_at(a, b, h, r0 + r).q + 8 * q : 0;
+      cp16(sm + L::Q + (r >> 7) * KB * L::QC + (q >> 3) * L::QC + swz(r & 127, q & 7), Q + src,
+           live ? 16 : 0);
+    }
+    cp_commit();
+    cp_wait<0>();
+    fence_async();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tbase = tslot;
+  bool ok = true;
+  auto wait = [&](uint64_t& bar, int use) { ok = ok && mbar_wait(smem_u32(&bar), (uint32_t)(use & 1)); };
+
+  if (warp >= 8 && warp < 12) {
+    // ---- loads -----------------------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+    const int lw = warp - 8;  // this warp's keys of a tile: 32 lw + lane
+    auto lookup = [&](int T) -> int {
+      const int t = t0 + T * kKeys + 32 * lw + lane;
+      return T < nt && t < t1 ? (int)row_of(a.c, b, h, t) : -1;
+    };
+    int signalled = 0, issued = 0;  // loads whose arrival was reported, and begun, in order
+    auto begin = [&](int item) {  // its stage is free
+      if (item >= NS) wait(mEmpty[item % NS], item / NS - 1);
+    };
+    auto report = [&](int item) {
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&mFull[item % NS]));
+    };
+    // bf16: copies run LAG loads ahead of their report
+    auto copy = [&](int item, const void* base, int row) {
+      begin(item);
+      unsigned char* st = sm + L::STAGES + (item % NS) * L::SS;
+      constexpr int LPR = D / 8, RPI = 32 / LPR;
+      const int q = lane % LPR;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(base) + 8 * q;
+#pragma unroll 8
+      for (int j = 0; j < 32 / RPI; ++j) {
+        const int r = j * RPI + lane / LPR;
+        const int pr = __shfl_sync(0xffffffffu, row, r);
+        cp16(st + (q >> 3) * L::QC + swz(32 * lw + r, q & 7), src + (long long)max(pr, 0) * D, pr < 0 ? 0 : 16);
+      }
+      cp_commit();
+    };
+    // 8-bit: the next load's rows wait in registers while this one's are converted
+    constexpr int LPR8 = D / 16, RPI8 = 32 / LPR8, N8 = 32 / RPI8;
+    uint4 w8[N8];
+    auto fetch = [&](const void* base, int row) {
+      const int q = lane % LPR8;
+      const unsigned char* src = static_cast<const unsigned char*>(base) + 16 * q;
+#pragma unroll
+      for (int j = 0; j < N8; ++j) {
+        const int pr = __shfl_sync(0xffffffffu, row, j * RPI8 + lane / LPR8);
+        w8[j] = make_uint4(0, 0, 0, 0);
+        if (pr >= 0) w8[j] = __ldg(reinterpret_cast<const uint4*>(src + (long long)pr * D));
+      }
+    };
+    auto convert = [&](int item) {
+      begin(item);
+      unsigned char* st = sm + L::STAGES + (item % NS) * L::SS;
+      const int q = 2 * (lane % LPR8);
+#pragma unroll
+      for (int j = 0; j < N8; ++j) {
+        const int r = 32 * lw + j * RPI8 + lane / LPR8;
+        const uint32_t w[4] = {w8[j].x, w8[j].y, w8[j].z, w8[j].w};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint4*>(st + (q >> 3) * L::QC + swz(r, (q & 7) + e)) =
+              make_uint4(bf16_of_bytes<CT>(w[2 * e], w[2 * e], 0, 1), bf16_of_bytes<CT>(w[2 * e], w[2 * e], 2, 3),
+                         bf16_of_bytes<CT>(w[2 * e + 1], w[2 * e + 1], 0, 1),
+                         bf16_of_bytes<CT>(w[2 * e + 1], w[2 * e + 1], 2, 3));
+      }
+    };
+    if (nt > 0) {
+      int rk = lookup(0), rv = rk;  // page rows of the next K and the next V
+      if (k8) {
+        fetch(a.c.k, rk);
+        for (int T = -1; T < nt; ++T) {
+          // K[T + 1] is in registers (if there is one); V[T] after it
+          float ks = 0.f, vs = 0.f;
+          if (T >= 0) {
+            if (rv >= 0) {
+              ks = a.c.ks[rv];
+              vs = a.c.vs[rv];
+            }
+          }
+          if (T + 1 < nt) {
+            convert(k_item(T + 1));
+            report(k_item(T + 1));
+          }
+          if (T >= 0) {
+            fetch(a.c.v, rv);
+            convert(v_item(T));
+            float* sc = reinterpret_cast<float*>(sm + L::SC) + (v_item(T) % NS) * 2 * kKeys + 32 * lw + lane;
+            sc[0] = ks;
+            sc[kKeys] = vs;
+            report(v_item(T));
+          }
+          rv = rk;
+          rk = lookup(T + 2);
+          if (T + 2 < nt) fetch(a.c.k, rk);
+        }
+      } else {
+        auto pump = [&]() {  // report the loads that LAG newer ones follow
+          ++issued;
+          if (issued > L::LAG) {
+            cp_wait<L::LAG>();
+            report(signalled);
+            ++signalled;
+          }
+        };
+        copy(k_item(0), a.c.k, rk);
+        pump();
+        for (int T = 0; T < nt; ++T) {
+          rv = rk;
+          rk = lookup(T + 1);
+          if (T + 1 < nt) {
+            copy(k_item(T + 1), a.c.k, rk);
+            pump();
+          }
+          copy(v_item(T), a.c.v, rv);
+          pump();
+        }
+        cp_wait<0>();
+        for (; signalled < 2 * nt; ++signalled) report(signalled);
+      }
+    }
+  } else if (warp >= 12) {
+    // ---- products --------------------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;\n");
+    if (warp == 12 && lane == 0) {
+      const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
+      const uint32_t id_pv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
+      auto stage = [&](int item) { return sb + L::STAGES + (item % NS) * L::SS; };
+      auto issue_s = [&](int w, int k) {
+        const int it = k_item(tile_at(w, k));
+        wait(mFull[it % NS], it / NS);
+        fence_after();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const uint64_t ad = desc_k(sb + L::Q + (two ? w : 0) * KB * L::QC + kb * L::QC);
+          const uint64_t bd = desc_k(stage(it) + kb * L::QC);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) umma(tbase + 128 * w, ad + 2 * q, bd + 2 * q, id_s, (kb | q) ? 1u : 0u);
+        }
+        umma_commit(smem_u32(&mS[w]));
+        if (!two || w == 1) umma_commit(smem_u32(&mEmpty[it % NS]));
+      };
+      auto issue_pv = [&](int w, int k) {
+        const int it = v_item(tile_at(w, k));
+        wait(mFull[it % NS], it / NS);
+        wait(mP[w], k);
+        fence_after();
+#pragma unroll
+        for (int q = 0; q < kKeys / 16; ++q)
+          umma_ts(tbase + 256 + D * w, tbase + 128 * w + 8 * q, desc_mn(stage(it) + 2048 * q, L::QC), id_pv,
+                  (k | q) ? 1u : 0u);
+        if (!two || w == 1) umma_commit(smem_u32(&mEmpty[it % NS]));
+        if (k + 1 == steps(w)) umma_commit(smem_u32(&mO[w]));
+      };
+      for (int w = 0; w < 2; ++w)
+        if (steps(w) > 0) issue_s(w, 0);
+      for (int k = 0; k < steps(0); ++k)
+        for (int w = 0; w < 2; ++w)
+          if (k < steps(w)) {
+            issue_pv(w, k);
+            if (k + 1 < steps(w)) issue_s(w, k + 1);
+          }
+    }
+  } else {
+    // ---- softmax: thread = row -------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n");
+    const int w = warp >> 2, row = tid & 127;
+    const int pr = r0 + (two ? 128 * w : 0) + row;  // packed row
+    const bool live = pr < rt.r1;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tbase + 128 * w + lanes, tO = tbase + 256 + D * w + lanes;
+    // what this row, and every row of the stream, sees
+    const int2 see = live ? seen(a, s, s.pos0 + pr / a.G) : make_int2(0, 0);
+    int alo = rt.alo, ahi = rt.ahi;
+    if (two) {
+      const int f = r0 + 128 * w, e = min(rt.r1, f + 128) - 1;
+      alo = seen(a, s, s.pos0 + e / a.G).x;
+      ahi = seen(a, s, s.pos0 + f / a.G).y;
+    }
+    float sl2 = a.scale * kLog2e;
+    const bool pos = sl2 > 0.f;
+    float m = kFloor, l = 0.f;
+    const int n = steps(w);
+    for (int k = 0; k < n; ++k) {
+      const int T = tile_at(w, k), tb = t0 + T * kKeys;
+      wait(mS[w], k);
+      fence_after();
+      uint32_t x[kKeys];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tld32(tS + 32 * q, x + 32 * q);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tld_wait(x + 32 * q);
+      const int vi = v_item(T);
+      const float* sc = reinterpret_cast<const float*>(sm + L::SC) + (vi % NS) * 2 * kKeys;
+      const bool edge = tb < alo || tb + kKeys > ahi || tb + kKeys > t1;
+      if (k8 || edge) wait(mFull[vi % NS], vi / NS);
+      if (k8) {
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(sc + c);
+          x[c] = __float_as_uint(__uint_as_float(x[c]) * f.x);
+          x[c + 1] = __float_as_uint(__uint_as_float(x[c + 1]) * f.y);
+          x[c + 2] = __float_as_uint(__uint_as_float(x[c + 2]) * f.z);
+          x[c + 3] = __float_as_uint(__uint_as_float(x[c + 3]) * f.w);
+        }
+      }
+      float mul = sl2;
+      if (!pos) {  // logits first: the largest product need not be the largest logit
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * sl2);
+        mul = 1.f;
+      }
+      const int clo = see.x - tb, chi = min(see.y, t1) - tb;
+      if (edge) {
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c)
+          if (c < clo || c >= chi) x[c] = 0xFF800000u;
+        if (CT != kCacheI8 && (tb < alo || tb + kKeys > ahi)) {
+          // values that are not numbers would reach the rows that do not see them
+          bool f = false;
+          const unsigned char* sv = sm + L::STAGES + (vi % NS) * L::SS;
+          for (int e = row; e < L::SS / 16; e += 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(sv + 16 * e);
+            f = f || bf16_not_finite(u.x) || bf16_not_finite(u.y) || bf16_not_finite(u.z) || bf16_not_finite(u.w);
+          }
+          if (f) sbad = 1;
+        }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+      const bool move = top > m + kSlack;
+      if (__any_sync(0xffffffffu, move)) {
+        const float f = move ? fast_exp2(m - top) : 1.f;
+        m = move ? top : m;
+        l *= f;
+        if (k > 0) {  // the stream's last P V is done: S came after it
+#pragma unroll
+          for (int d = 0; d < D; d += 32) {
+            uint32_t r[32];
+            tld32(tO + d, r);
+            tld_wait(r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+            tst32(tO + d, r);
+          }
+        }
+      }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t p[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int c = 64 * q + 2 * e;
+          float y0 = fast_exp2(fmaf(__uint_as_float(x[c]), mul, -m));
+          float y1 = fast_exp2(fmaf(__uint_as_float(x[c + 1]), mul, -m));
+          sum[2 * (e & 1)] += y0;
+          sum[2 * (e & 1) + 1] += y1;
+          if (k8) {
+            const float2 f = *reinterpret_cast<const float2*>(sc + kKeys + c);
+            y0 *= f.x;
+            y1 *= f.y;
+            if (edge) {  // a masked key's scale need not be a number
+              y0 = c < clo || c >= chi ? 0.f : y0;
+              y1 = c + 1 < clo || c + 1 >= chi ? 0.f : y1;
+            }
+          }
+          p[e] = bf16_bits2(y0, y1);
+        }
+        tst32(tS + 32 * q, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tst_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&mP[w]));
+    }
+    if (n > 0) {
+      wait(mO[w], 0);
+      fence_after();
+    }
+    if (!ok) sfail = 1;
+
+    // ---- the rows: joined streams, normalised (or a split's partial) --------------
+    float* jo = reinterpret_cast<float*>(sm + L::STAGES);  // [column][row]; every load was used
+    if (!two) {
+      streams_sync();  // both streams' products are done
+      if (w == 1 && n > 0) {
+#pragma unroll
+        for (int d = 0; d < D; d += 32) {
+          uint32_t r[32];
+          tld32(tO + d, r);
+          tld_wait(r);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) jo[(d + e) * 128 + row] = __uint_as_float(r[e]);
+        }
+        jml[row] = make_float2(m, l);
+      }
+      streams_sync();
+    }
+    const bool join = !two && steps(1) > 0;
+    if (two || w == 0) {
+      float f0 = 1.f, f1 = 0.f;
+      if (join) {
+        const float2 ml = jml[row];
+        const float mn = fmaxf(m, ml.x);
+        f0 = fast_exp2(m - mn);
+        f1 = fast_exp2(ml.x - mn);
+        m = mn;
+        l = l * f0 + ml.y * f1;
+      }
+      const RowAt at = row_at(a, b, h, live ? pr : r0);
+      const float inv = parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.O) + at.o;
+#pragma unroll
+      for (int d = 0; d < D; d += 32) {
+        uint32_t r[32];
+        if (n > 0) {
+          tld32(tO + d, r);
+          tld_wait(r);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0;
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            y[e] = __uint_as_float(r[8 * c + e]);
+            if (join) y[e] = y[e] * f0 + jo[(d + 8 * c + e) * 128 + row] * f1;
+            y[e] *= inv;
+          }
+          if (parts > 1)
+            store8(part_o<D>(a, tile, split, pr - r0) + d + 8 * c, y);
+          else
+            store8(op + d + 8 * c, y);
+        }
+      }
+      if (live) {
+        if (parts > 1)
+          *part_ml(a, tile, split, pr - r0) = make_float2(m, l);
+        else if (a.lse)
+          a.lse[at.lse] = lse_of(m, l);
+      }
+    }
+    streams_sync();
+    if (sbad)
+      for (int r = r0 + warp; r < rt.r1; r += 8)
+        redo_row<__nv_bfloat16, CT, D>(a, s, b, h, r, t0, t1, tile, split, parts, r0);
+  }
+  if (!ok) sfail = 1;
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (tid == 0 && sfail && a.c.err) atomicOr(a.c.err, kErrMmaWait);
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tbase));
+}
+
+template <int CT, int D>
+void launch(const CacheAttn& a, cudaStream_t st) {
+  const int smem = ChunkL<CT, D>::TOTAL;
+  cudaFuncSetAttribute(cache_chunk_kernel<CT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const long long blocks = (long long)a.B * a.c.Hkv * a.RT * a.S;
+  cache_chunk_kernel<CT, D><<<(unsigned)blocks, kThreads, smem, st>>>(a);
+}
+
+}  // namespace
+
+void run_cache_chunk(const CacheAttn& a, cudaStream_t st) {
+  ProfScope ps(st, "cache_chunk");
+  switch (a.type * 2 + (a.c.D == 128)) {
+    case 2 * kCacheBf16: return launch<kCacheBf16, 64>(a, st);
+    case 2 * kCacheBf16 + 1: return launch<kCacheBf16, 128>(a, st);
+    case 2 * kCacheE4m3: return launch<kCacheE4m3, 64>(a, st);
+    case 2 * kCacheE4m3 + 1: return launch<kCacheE4m3, 128>(a, st);
+    case 2 * kCacheI8: return launch<kCacheI8, 64>(a, st);
+    default: return launch<kCacheI8, 128>(a, st);
+  }
+}
+
+}  // namespace muse

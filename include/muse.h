@@ -389,7 +389,7 @@ typedef enum {
 typedef struct {
   void *k, *v;
   float *k_scale, *v_scale;
-  int pages, page_size; /* any page_size >= 1 */
+  int pages, page_size; /* any page_size >= 1; pages * Hkv * page_size < 2^31 */
   muse_cache_dtype dtype;
 } muse_cache;
 

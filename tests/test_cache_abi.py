@@ -171,3 +171,15 @@ def test_plain_attention_is_softmax_attention():
         assert np.allclose(o[b], want.numpy(), atol=1e-12)
         x = (0.2 * q[b].double() @ K.transpose(1, 2)).masked_fill(~mask, -torch.inf)
         assert np.allclose(lse[b], torch.logsumexp(x, -1).numpy(), atol=1e-12)
+
+
+@pytest.mark.parametrize("call", ["write", "read", "attend"])
+def test_more_rows_than_an_index_holds(lib, call):
+    """2^31 page rows of a head dimension of 64 are more than 256 GB of K and V."""
+    ca, ix, sh = cache(pages=1 << 26, page=16), index(), shape()
+    args = dict(write=(FAKE, strides(), FAKE, strides(), sh, ca, ix, None, None),
+                read=(FAKE, FAKE, sh, ca, ix, None, None, None),
+                attend=(FAKE, strides(), FAKE, strides(), None, sh, ca, ix, 1.0, 1, 0, None, FAKE, 1, None))
+    f = getattr(lib, "muse_attn_cache" if call == "attend" else "muse_cache_" + call)
+    assert f(*args[call]) == 2 and b"2^31" in lib.muse_last_error()
+    assert lib.muse_attn_cache_workspace_size(sh, ca, ix) == 0
