@@ -21,6 +21,8 @@
 // columns.
 //
 // Warps 0-7: softmax of stream 0 (0-3) and 1 (4-7); 8-11: loads; 12: products.
+// One warp issues all products, the streams in turn: that keeps them half a
+// step apart (two issuing warps drift into step, softmax against softmax).
 // Every wait is bounded; one that gives up sets kErrMmaWait.
 #include "cache_attn.cuh"
 #include "kernels.h"
@@ -33,7 +35,7 @@ namespace {
 constexpr int kKeys = 128;    // keys of a tile
 constexpr int kThreads = 512;
 constexpr int kLoad = 128;    // load threads
-// Registers a thread: 256 softmax x 200 + 128 load x 80 + 128 product x 32
+// Registers a thread: 256 softmax x 192 + 128 load x 80 + 128 product x 48
 // = the 512 x 128 of the launch.
 
 __device__ inline int swz(int r, int q) { return r * 128 + ((q ^ (r & 7)) << 4); }
@@ -65,11 +67,26 @@ __device__ inline void umma_commit(uint32_t mbar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(mbar)
                : "memory");
 }
+__device__ inline bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
+  return e != 0;
+}
 __device__ inline void mbar_init(uint32_t mbar, int count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(mbar), "r"(count));
 }
 __device__ inline void mbar_arrive(uint32_t mbar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(mbar) : "memory");
+}
+__device__ inline bool mbar_test(uint32_t mbar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(mbar), "r"(parity)
+      : "memory");
+  return done != 0;
 }
 // Bounded wait for the phase of this parity; false when it gave up.
 __device__ inline bool mbar_wait(uint32_t mbar, uint32_t parity) {
@@ -106,6 +123,37 @@ __device__ inline void tst32(uint32_t taddr, const uint32_t* r) {
       "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ inline void tst16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Two fp32 at a time: r[0..1] *= (a, b); r[0..1] = r a + b; s += r.
+__device__ inline void mul2(uint32_t* r, float a, float b) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "+r"(r[0]), "+r"(r[1])
+      : "f"(a), "f"(b));
+}
+__device__ inline void fma2(uint32_t* r, float a, float b) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "+r"(r[0]), "+r"(r[1])
+      : "f"(a), "f"(b));
+}
+__device__ inline void add2(uint64_t& s, const uint32_t* r) {
+  asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tadd.rn.f32x2 %0, %0, x;\n\t}\n"
+      : "+l"(s)
+      : "r"(r[0]), "r"(r[1]));
+}
+__device__ inline float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 // The wait for this thread's TMEM loads, tied to their registers so that no
 // use of them moves above it.
 __device__ inline void tld_wait(uint32_t* r) {
@@ -131,10 +179,13 @@ struct ChunkL {
   static constexpr int Q = 0;                 // [stream][chunk][128 rows][128 B]
   static constexpr int STAGES = Q + 2 * KB * QC;
   static constexpr int SS = KB * QC;          // one tile of K or V
-  static constexpr int NS = D == 128 ? (CT == kCacheBf16 ? 5 : 4) : 8;
-  static constexpr int LAG = NS == 8 ? 4 : NS - 2;  // copies in flight; load i waits for load i - NS's stage
+  static constexpr int NS = CT == kCacheBf16 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);
+  static constexpr int LAG = NS - 2;  // copies on their way while stages are free
   static constexpr int SC = STAGES + NS * SS;  // 8-bit: (k, v) scales [stage][2][128], with V
-  static constexpr int TOTAL = SC + (CT == kCacheBf16 ? 0 : NS * 2 * kKeys * 4) + 1024;
+  static constexpr int RS = D == 128 ? 3 : 6;  // 8-bit: raw loads on their way, and the bytes of
+  static constexpr int RAWW = 32 * D + 32 * 8;  // a load warp's share of one (rows, scales)
+  static constexpr int RAW = SC + (CT == kCacheBf16 ? 0 : NS * 2 * kKeys * 4);
+  static constexpr int TOTAL = RAW + (CT == kCacheBf16 ? 0 : 4 * RS * RAWW) + 1024;
 };
 
 template <int CT, int D>
@@ -169,11 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
   auto tile_at = [&](int w, int k) { return two ? k : 2 * k + w; };
   // loads in the order of their use: K0, K1, V0, K2, V1, ... K[nt - 1], V[nt - 2],
   // V[nt - 1]; the number of a load is its place in that order.  The stage of
-  // load i is freed by products that need no load past i + 1.
+  // load i is freed by products that wait for no load past i + 1.
   auto k_item = [](int t) { return t == 0 ? 0 : 2 * t - 1; };
   auto v_item = [&](int t) { return min(2 * t + 2, 2 * nt - 1); };
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tslot)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
@@ -220,18 +271,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       const int t = t0 + T * kKeys + 32 * lw + lane;
       return T < nt && t < t1 ? (int)row_of(a.c, b, h, t) : -1;
     };
-    int signalled = 0, issued = 0;  // loads whose arrival was reported, and begun, in order
-    auto begin = [&](int item) {  // its stage is free
-      if (item >= NS) wait(mEmpty[item % NS], item / NS - 1);
-    };
     auto report = [&](int item) {
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&mFull[item % NS]));
     };
-    // bf16: copies run LAG loads ahead of their report
+    auto begin = [&](int item) {  // its stage is free
+      if (item >= NS) wait(mEmpty[item % NS], item / NS - 1);
+    };
+    // bf16: while stages are free, copies run LAG loads ahead of the report of
+    // their arrival; before a wait for a stage every arrival is reported
+    int signalled = 0, issued = 0;
+    auto report_to = [&](int end) {
+      for (; signalled < end; ++signalled) report(signalled);
+    };
     auto copy = [&](int item, const void* base, int row) {
-      begin(item);
+      if (item >= NS && !__all_sync(0xffffffffu, mbar_test(smem_u32(&mEmpty[item % NS]), (item / NS - 1) & 1))) {
+        cp_wait<0>();
+        report_to(issued);
+        begin(item);
+      }
       unsigned char* st = sm + L::STAGES + (item % NS) * L::SS;
       constexpr int LPR = D / 8, RPI = 32 / LPR;
       const int q = lane % LPR;
@@ -244,27 +303,46 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       }
       cp_commit();
     };
-    // 8-bit: the next load's rows wait in registers while this one's are converted
+    // 8-bit: the raw rows of the next RS loads are on their way to a ring of this
+    // thread's own (it converts the bytes that it copied)
     constexpr int LPR8 = D / 16, RPI8 = 32 / LPR8, N8 = 32 / RPI8;
-    uint4 w8[N8];
-    auto fetch = [&](const void* base, int row) {
-      const int q = lane % LPR8;
-      const unsigned char* src = static_cast<const unsigned char*>(base) + 16 * q;
+    unsigned char* raw = sm + L::RAW + lw * (L::RS * L::RAWW);
+    int fetched = 0, row_next = k8 ? lookup(0) : -1, row_cur = -1, row_prev = -1;
+    auto is_k = [&](int item) { return item == 0 || ((item & 1) && item < 2 * nt - 1); };
+    auto fetch = [&]() {
+      if (fetched < 2 * nt) {
+        const bool k = is_k(fetched);
+        if (k) {
+          row_prev = row_cur;
+          row_cur = row_next;
+          row_next = lookup((fetched + 1) / 2 + 1);
+        }
+        // V[t] follows K[t + 1], the last V its own K
+        const int row = k || fetched == 2 * nt - 1 ? row_cur : row_prev;
+        unsigned char* dst = raw + (fetched % L::RS) * L::RAWW;
+        const unsigned char* src = static_cast<const unsigned char*>(k ? a.c.k : a.c.v) + 16 * (lane % LPR8);
 #pragma unroll
-      for (int j = 0; j < N8; ++j) {
-        const int pr = __shfl_sync(0xffffffffu, row, j * RPI8 + lane / LPR8);
-        w8[j] = make_uint4(0, 0, 0, 0);
-        if (pr >= 0) w8[j] = __ldg(reinterpret_cast<const uint4*>(src + (long long)pr * D));
+        for (int j = 0; j < N8; ++j) {
+          const int pr = __shfl_sync(0xffffffffu, row, j * RPI8 + lane / LPR8);
+          cp16(dst + (j * 32 + lane) * 16, src + (long long)max(pr, 0) * D, pr < 0 ? 0 : 16);
+        }
+        if (!k) {
+          cp4(dst + 32 * D + 8 * lane, a.c.ks + max(row, 0), row < 0 ? 0 : 4);
+          cp4(dst + 32 * D + 8 * lane + 4, a.c.vs + max(row, 0), row < 0 ? 0 : 4);
+        }
       }
+      ++fetched;
+      cp_commit();
     };
     auto convert = [&](int item) {
-      begin(item);
+      const unsigned char* from = raw + (item % L::RS) * L::RAWW;
       unsigned char* st = sm + L::STAGES + (item % NS) * L::SS;
       const int q = 2 * (lane % LPR8);
 #pragma unroll
       for (int j = 0; j < N8; ++j) {
         const int r = 32 * lw + j * RPI8 + lane / LPR8;
-        const uint32_t w[4] = {w8[j].x, w8[j].y, w8[j].z, w8[j].w};
+        const uint4 u = *reinterpret_cast<const uint4*>(from + (j * 32 + lane) * 16);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           *reinterpret_cast<uint4*>(st + (q >> 3) * L::QC + swz(r, (q & 7) + e)) =
@@ -272,44 +350,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
                          bf16_of_bytes<CT>(w[2 * e + 1], w[2 * e + 1], 0, 1),
                          bf16_of_bytes<CT>(w[2 * e + 1], w[2 * e + 1], 2, 3));
       }
+      if (!is_k(item)) {
+        float* sc = reinterpret_cast<float*>(sm + L::SC) + (item % NS) * 2 * kKeys + 32 * lw + lane;
+        const float2 f = *reinterpret_cast<const float2*>(from + 32 * D + 8 * lane);
+        sc[0] = f.x;
+        sc[kKeys] = f.y;
+      }
     };
     if (nt > 0) {
-      int rk = lookup(0), rv = rk;  // page rows of the next K and the next V
       if (k8) {
-        fetch(a.c.k, rk);
-        for (int T = -1; T < nt; ++T) {
-          // K[T + 1] is in registers (if there is one); V[T] after it
-          float ks = 0.f, vs = 0.f;
-          if (T >= 0) {
-            if (rv >= 0) {
-              ks = a.c.ks[rv];
-              vs = a.c.vs[rv];
-            }
-          }
-          if (T + 1 < nt) {
-            convert(k_item(T + 1));
-            report(k_item(T + 1));
-          }
-          if (T >= 0) {
-            fetch(a.c.v, rv);
-            convert(v_item(T));
-            float* sc = reinterpret_cast<float*>(sm + L::SC) + (v_item(T) % NS) * 2 * kKeys + 32 * lw + lane;
-            sc[0] = ks;
-            sc[kKeys] = vs;
-            report(v_item(T));
-          }
-          rv = rk;
-          rk = lookup(T + 2);
-          if (T + 2 < nt) fetch(a.c.k, rk);
+        for (int i = 0; i < L::RS - 1; ++i) fetch();
+        for (int item = 0; item < 2 * nt; ++item) {
+          fetch();
+          cp_wait<L::RS - 1>();
+          begin(item);
+          convert(item);
+          report(item);
         }
       } else {
-        auto pump = [&]() {  // report the loads that LAG newer ones follow
+        int rk = lookup(0), rv = rk;  // page rows of the next K and the next V
+        auto pump = [&]() {
           ++issued;
-          if (issued > L::LAG) {
-            cp_wait<L::LAG>();
-            report(signalled);
-            ++signalled;
-          }
+          cp_wait<L::LAG>();
+          report_to(issued - L::LAG);
         };
         copy(k_item(0), a.c.k, rk);
         pump();
@@ -324,54 +387,75 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           pump();
         }
         cp_wait<0>();
-        for (; signalled < 2 * nt; ++signalled) report(signalled);
+        report_to(2 * nt);
       }
     }
   } else if (warp >= 12) {
     // ---- products --------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;\n");
-    if (warp == 12 && lane == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
+    if (warp == 12) {
+      // The whole warp walks the loop and one elected lane issues: operands stay in
+      // uniform registers (a lane's own branch costs about 40 cycles a product).
       const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
       const uint32_t id_pv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
-      auto stage = [&](int item) { return sb + L::STAGES + (item % NS) * L::SS; };
-      auto issue_s = [&](int w, int k) {
-        const int it = k_item(tile_at(w, k));
-        wait(mFull[it % NS], it / NS);
-        fence_after();
+      const uint64_t qd = desc_k(sb + L::Q), kd = desc_k(sb + L::STAGES), vd = desc_mn(sb + L::STAGES, L::QC);
+      const int unt = __shfl_sync(0xffffffffu, nt, 0);
+      const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+      const bool both = __shfl_sync(0xffffffffu, (int)two, 0) != 0;
+      const int n0 = both ? unt : (unt + 1) >> 1, n1 = both ? unt : unt >> 1;
+      auto issue_s = [&](int w, int item) {
+        const int st = item % NS;
+        const uint64_t ad = qd + (both ? w : 0) * (KB * L::QC >> 4), bd = kd + st * (L::SS >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const uint64_t ad = desc_k(sb + L::Q + (two ? w : 0) * KB * L::QC + kb * L::QC);
-          const uint64_t bd = desc_k(stage(it) + kb * L::QC);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) umma(tbase + 128 * w, ad + 2 * q, bd + 2 * q, id_s, (kb | q) ? 1u : 0u);
+          for (int q = 0; q < 4 * KB; ++q) {
+            const uint32_t at = (q >> 2) * (L::QC >> 4) + 2 * (q & 3);
+            umma(tb + 128 * w, ad + at, bd + at, id_s, q ? 1u : 0u);
+          }
+          umma_commit(smem_u32(&mS[w]));
+          if (!both || w == 1) umma_commit(smem_u32(&mEmpty[st]));
         }
-        umma_commit(smem_u32(&mS[w]));
-        if (!two || w == 1) umma_commit(smem_u32(&mEmpty[it % NS]));
-      };
-      auto issue_pv = [&](int w, int k) {
-        const int it = v_item(tile_at(w, k));
-        wait(mFull[it % NS], it / NS);
-        wait(mP[w], k);
-        fence_after();
-#pragma unroll
-        for (int q = 0; q < kKeys / 16; ++q)
-          umma_ts(tbase + 256 + D * w, tbase + 128 * w + 8 * q, desc_mn(stage(it) + 2048 * q, L::QC), id_pv,
-                  (k | q) ? 1u : 0u);
-        if (!two || w == 1) umma_commit(smem_u32(&mEmpty[it % NS]));
-        if (k + 1 == steps(w)) umma_commit(smem_u32(&mO[w]));
+        __syncwarp();
       };
       for (int w = 0; w < 2; ++w)
-        if (steps(w) > 0) issue_s(w, 0);
-      for (int k = 0; k < steps(0); ++k)
-        for (int w = 0; w < 2; ++w)
-          if (k < steps(w)) {
-            issue_pv(w, k);
-            if (k + 1 < steps(w)) issue_s(w, k + 1);
+        if ((w ? n1 : n0) > 0) {
+          const int it = k_item(both ? 0 : w);
+          wait(mFull[it % NS], it / NS);
+          fence_after();
+          issue_s(w, it);
+        }
+#pragma unroll 1
+      for (int k = 0; k < n0; ++k) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {  // step k of stream 0, then of stream 1
+          const int n = w ? n1 : n0;
+          if (k >= n) break;
+          // the operands first, so that nothing stands between P V and the next S
+          const int T = both ? k : 2 * k + w, more = k + 1 < n;
+          const int vi = min(2 * T + 2, 2 * unt - 1), ki = more ? 2 * (both ? T + 1 : T + 2) - 1 : vi;
+          const int vst = vi % NS;
+          if (!both || w == 0) {
+            wait(mFull[vst], vi / NS);
+            wait(mFull[ki % NS], ki / NS);
           }
+          wait(mP[w], k);
+          fence_after();
+          if (elect_one()) {
+            const uint64_t bd = vd + vst * (L::SS >> 4);
+#pragma unroll
+            for (int q = 0; q < kKeys / 16; ++q)
+              umma_ts(tb + 256 + D * w, tb + 128 * w + 8 * q, bd + 128 * q, id_pv, (k | q) ? 1u : 0u);
+            if (!both || w == 1) umma_commit(smem_u32(&mEmpty[vst]));
+            if (!more) umma_commit(smem_u32(&mO[w]));
+          }
+          __syncwarp();
+          if (more) issue_s(w, ki);
+        }
+      }
     }
   } else {
     // ---- softmax: thread = row -------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n");
     const int w = warp >> 2, row = tid & 127;
     const int pr = r0 + (two ? 128 * w : 0) + row;  // packed row
     const bool live = pr < rt.r1;
@@ -385,8 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       alo = seen(a, s, s.pos0 + e / a.G).x;
       ahi = seen(a, s, s.pos0 + f / a.G).y;
     }
-    float sl2 = a.scale * kLog2e;
+    const float sl2 = a.scale * kLog2e;
     const bool pos = sl2 > 0.f;
+    const float mul = pos ? sl2 : 1.f;
     float m = kFloor, l = 0.f;
     const int n = steps(w);
     for (int k = 0; k < n; ++k) {
@@ -406,17 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
 #pragma unroll
         for (int c = 0; c < kKeys; c += 4) {
           const float4 f = *reinterpret_cast<const float4*>(sc + c);
-          x[c] = __float_as_uint(__uint_as_float(x[c]) * f.x);
-          x[c + 1] = __float_as_uint(__uint_as_float(x[c + 1]) * f.y);
-          x[c + 2] = __float_as_uint(__uint_as_float(x[c + 2]) * f.z);
-          x[c + 3] = __float_as_uint(__uint_as_float(x[c + 3]) * f.w);
+          mul2(x + c, f.x, f.y);
+          mul2(x + c + 2, f.z, f.w);
         }
       }
-      float mul = sl2;
       if (!pos) {  // logits first: the largest product need not be the largest logit
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * sl2);
-        mul = 1.f;
+        for (int c = 0; c < kKeys; c += 2) mul2(x + c, sl2, sl2);
       }
       const int clo = see.x - tb, chi = min(see.y, t1) - tb;
       if (edge) {
@@ -436,50 +517,61 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+      for (int c = 0; c < kKeys; c += 2)
+        mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+      const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * mul;
       const bool move = top > m + kSlack;
       if (__any_sync(0xffffffffu, move)) {
         const float f = move ? fast_exp2(m - top) : 1.f;
         m = move ? top : m;
         l *= f;
         if (k > 0) {  // the stream's last P V is done: S came after it
-#pragma unroll
+#pragma unroll 1
           for (int d = 0; d < D; d += 32) {
             uint32_t r[32];
             tld32(tO + d, r);
             tld_wait(r);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+            for (int e = 0; e < 32; e += 2) mul2(r + e, f, f);
             tst32(tO + d, r);
           }
         }
       }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t p[32];
+      for (int q = 0; q < 4; ++q) {
+        uint32_t p[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int c = 64 * q + 2 * e;
-          float y0 = fast_exp2(fmaf(__uint_as_float(x[c]), mul, -m));
-          float y1 = fast_exp2(fmaf(__uint_as_float(x[c + 1]), mul, -m));
-          sum[2 * (e & 1)] += y0;
-          sum[2 * (e & 1) + 1] += y1;
-          if (k8) {
-            const float2 f = *reinterpret_cast<const float2*>(sc + kKeys + c);
-            y0 *= f.x;
-            y1 *= f.y;
-            if (edge) {  // a masked key's scale need not be a number
-              y0 = c < clo || c >= chi ? 0.f : y0;
-              y1 = c + 1 < clo || c + 1 >= chi ? 0.f : y1;
-            }
-          }
-          p[e] = bf16_bits2(y0, y1);
+        for (int e = 0; e < 16; ++e) {
+          const int c = 32 * q + 2 * e;
+          fma2(x + c, mul, -m);
+          x[c] = __float_as_uint(fast_exp2(__uint_as_float(x[c])));
+          x[c + 1] = __float_as_uint(fast_exp2(__uint_as_float(x[c + 1])));
+          add2(sum[e & 1], x + c);
+          if (!k8) p[e] = bf16_bits2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
         }
-        tst32(tS + 32 * q, p);
+        if (k8) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const int c = 32 * q + 2 * e;
+            const float4 f = *reinterpret_cast<const float4*>(sc + kKeys + c);
+            mul2(x + c, f.x, f.y);
+            mul2(x + c + 2, f.z, f.w);
+          }
+          if (edge) {  // a masked key's scale need not be a number
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * q + e < clo || 32 * q + e >= chi) x[32 * q + e] = 0;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            p[e] = bf16_bits2(__uint_as_float(x[32 * q + 2 * e]), __uint_as_float(x[32 * q + 2 * e + 1]));
+        }
+        tst16(tS + 16 * q, p);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const uint32_t odd[2] = {(uint32_t)sum[1], (uint32_t)(sum[1] >> 32)};
+      add2(sum[0], odd);
+      l += __uint_as_float((uint32_t)sum[0]) + __uint_as_float((uint32_t)(sum[0] >> 32));
       tst_wait();
       fence_before();
       __syncwarp();

@@ -55,11 +55,6 @@ __device__ inline int at16(int r, int c) {
   return slot * 64 + ((c ^ (((r >> 2) & 1) << 1)) << 4);
 }
 
-__device__ inline void cp4(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(bytes));
-}
-
 template <int CT, int D>
 __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_constant__ CacheAttn a) {
   using L = StepL<CT, D>;
