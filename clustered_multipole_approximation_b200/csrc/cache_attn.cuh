@@ -7,6 +7,8 @@
 // tile of them, and the rows of a tile end at neighbouring positions.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "cache.cuh"
 
 namespace muse {
@@ -170,6 +172,27 @@ __device__ inline uint32_t bf16_of_bytes(uint32_t x, uint32_t y, int i, int j) {
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&p),
                                    *reinterpret_cast<const __nv_bfloat162*>(&n));
   return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// The same as an fp16 pair, bytes i and i + 1 of x: e4m3 by the hardware
+// conversion, int8 from the bits of 1024 + 128 + q.
+template <int CT>
+__device__ inline uint32_t half_of_bytes(uint32_t x, int i) {
+  if (CT == kCacheE4m3) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> (8 * i)), __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+  }
+  const uint32_t w = __byte_perm(x ^ 0x80808080u, 0x64646464u, i | 0x40 | ((i + 1) << 8) | 0x4000);
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&w), __floats2half2_rn(1152.f, 1152.f));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+// Powers of two (f, 1 / f) with f top in [2^14, 2^15), f at most 2^103 (1 / f
+// times a softmax scale stays a normal number); (1, 1) where top is not finite.
+__device__ inline float2 half_factor(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent
+  if (e == 255) return make_float2(1.f, 1.f);
+  const int n = min(127 + 14 - (e - 127), 127 + 103);
+  return make_float2(__uint_as_float((uint32_t)n << 23), __uint_as_float((uint32_t)(254 - n) << 23));
 }
 
 // Whether a word of stored values (two bf16, or four e4m3) holds one that is

@@ -28,11 +28,17 @@
 #include "kernels.h"
 #include "mma_sync.cuh"
 
+#include <type_traits>
+
 namespace muse {
 
 namespace {
 
 constexpr int kKeys = 128;    // keys of a tile
+// Scales of a tile come with its K and are read until its softmax ends.  K[t + 8]
+// is loaded after load 2 t + 9 or a later one was freed (at most 6 stages), which
+// P V of tile t precedes.
+constexpr int kScales = 8;
 constexpr int kThreads = 512;
 constexpr int kLoad = 128;    // load threads
 // Registers a thread: 256 softmax x 192 + 128 load x 80 + 128 product x 48
@@ -88,9 +94,11 @@ __device__ inline bool mbar_test(uint32_t mbar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// Bounded wait for the phase of this parity; false when it gave up.
-__device__ inline bool mbar_wait(uint32_t mbar, uint32_t parity) {
-  for (int it = 0; it < (1 << 22); ++it) {
+// Bounded wait for the phase of this parity: false when it gave up, after half
+// a second or because another wait of the CTA did.
+__device__ inline bool mbar_wait(uint32_t mbar, uint32_t parity, volatile int* fail) {
+  uint64_t start = 0;
+  for (int it = 0; it < (1 << 24); ++it) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
@@ -99,7 +107,14 @@ __device__ inline bool mbar_wait(uint32_t mbar, uint32_t parity) {
         : "r"(mbar), "r"(parity)
         : "memory");
     if (done) return true;
+    if ((it & 63) == 63) {
+      uint64_t now;
+      asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(now));
+      if (start == 0) start = now;
+      if (*fail || now - start > 500000000ull) break;
+    }
   }
+  *fail = 1;
   return false;
 }
 __device__ inline void tld32(uint32_t taddr, uint32_t* r) {
@@ -181,10 +196,10 @@ struct ChunkL {
   static constexpr int SS = KB * QC;          // one tile of K or V
   static constexpr int NS = CT == kCacheBf16 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);
   static constexpr int LAG = NS - 2;  // copies on their way while stages are free
-  static constexpr int SC = STAGES + NS * SS;  // 8-bit: (k, v) scales [stage][2][128], with V
+  static constexpr int SC = STAGES + NS * SS;  // 8-bit: (k, v) scales [tile % kScales][2][128]
   static constexpr int RS = D == 128 ? 3 : 6;  // 8-bit: raw loads on their way, and the bytes of
   static constexpr int RAWW = 32 * D + 32 * 8;  // a load warp's share of one (rows, scales)
-  static constexpr int RAW = SC + (CT == kCacheBf16 ? 0 : NS * 2 * kKeys * 4);
+  static constexpr int RAW = SC + (CT == kCacheBf16 ? 0 : kScales * 2 * kKeys * 4);
   static constexpr int TOTAL = RAW + (CT == kCacheBf16 ? 0 : 4 * RS * RAWW) + 1024;
 };
 
@@ -196,10 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
   extern __shared__ __align__(1024) unsigned char chunk_raw[];
   unsigned char* sm = chunk_raw + ((1024 - (smem_u32(chunk_raw) & 1023)) & 1023);
   const uint32_t sb = smem_u32(sm);
-  __shared__ __align__(8) uint64_t mFull[NS], mEmpty[NS], mS[2], mP[2], mO[2];
+  __shared__ __align__(8) uint64_t mFull[NS], mEmpty[NS], mS[2], mP[2][2], mO[2];
   __shared__ uint32_t tslot;
   __shared__ int sbad, sfail;
   __shared__ float2 jml[128];
+  __shared__ float qback[k8 ? 256 : 1];  // 8-bit: the power of two that undoes a row's factor
 
   const long long tile = blockIdx.x / a.S;
   const int split = (int)(blockIdx.x - tile * a.S);
@@ -235,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       }
       for (int w = 0; w < 2; ++w) {
         mbar_init(smem_u32(&mS[w]), 1);
-        mbar_init(smem_u32(&mP[w]), 4);
+        mbar_init(smem_u32(&mP[w][0]), 4);
+        mbar_init(smem_u32(&mP[w][1]), 4);
         mbar_init(smem_u32(&mO[w]), 1);
       }
       sbad = sfail = 0;
@@ -249,8 +266,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       const int r = e / P, q = e % P;
       const bool live = r0 + r < rt.r1;
       const long long src = live ? row_at(a, b, h, r0 + r).q + 8 * q : 0;
-      cp16(sm + L::Q + (r >> 7) * KB * L::QC + (q >> 3) * L::QC + swz(r & 127, q & 7), Q + src,
-           live ? 16 : 0);
+      unsigned char* dst = sm + L::Q + (r >> 7) * KB * L::QC + (q >> 3) * L::QC + swz(r & 127, q & 7);
+      if (!k8) {
+        cp16(dst, Q + src, live ? 16 : 0);
+      } else {
+        // fp16 for the fp16 form of an 8-bit K, the row brought to a maximum in
+        // [2^14, 2^15) by a power of two: exact for values down to 2^-31 of it
+        const uint4 v = live ? *reinterpret_cast<const uint4*>(Q + src) : make_uint4(0, 0, 0, 0);
+        float x[8];
+        load8_in(reinterpret_cast<const __nv_bfloat16*>(&v), x);
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+        for (int o = P / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float2 f = half_factor(top);
+        *reinterpret_cast<uint4*>(dst) =
+            make_uint4(pack_h2(x[0] * f.x, x[1] * f.x), pack_h2(x[2] * f.x, x[3] * f.x),
+                       pack_h2(x[4] * f.x, x[5] * f.x), pack_h2(x[6] * f.x, x[7] * f.x));
+        if (q == 0) qback[r] = f.y;
+      }
     }
     cp_commit();
     cp_wait<0>();
@@ -261,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
   fence_after();
   const uint32_t tbase = tslot;
   bool ok = true;
-  auto wait = [&](uint64_t& bar, int use) { ok = ok && mbar_wait(smem_u32(&bar), (uint32_t)(use & 1)); };
+  auto wait = [&](uint64_t& bar, int use) { ok = ok && mbar_wait(smem_u32(&bar), (uint32_t)(use & 1), &sfail); };
 
   if (warp >= 8 && warp < 12) {
     // ---- loads -----------------------------------------------------------------
@@ -326,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           const int pr = __shfl_sync(0xffffffffu, row, j * RPI8 + lane / LPR8);
           cp16(dst + (j * 32 + lane) * 16, src + (long long)max(pr, 0) * D, pr < 0 ? 0 : 16);
         }
-        if (!k) {
+        if (k) {
           cp4(dst + 32 * D + 8 * lane, a.c.ks + max(row, 0), row < 0 ? 0 : 4);
           cp4(dst + 32 * D + 8 * lane + 4, a.c.vs + max(row, 0), row < 0 ? 0 : 4);
         }
@@ -334,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       ++fetched;
       cp_commit();
     };
-    auto convert = [&](int item) {
+    auto convert = [&](int item, auto is_key) {
+      constexpr bool K = decltype(is_key)::value;
       const unsigned char* from = raw + (item % L::RS) * L::RAWW;
       unsigned char* st = sm + L::STAGES + (item % NS) * L::SS;
       const int q = 2 * (lane % LPR8);
@@ -343,15 +379,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         const int r = 32 * lw + j * RPI8 + lane / LPR8;
         const uint4 u = *reinterpret_cast<const uint4*>(from + (j * 32 + lane) * 16);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[2 * e] = K ? half_of_bytes<CT>(w[e], 0) : bf16_of_bytes<CT>(w[e], w[e], 0, 1);
+          y[2 * e + 1] = K ? half_of_bytes<CT>(w[e], 2) : bf16_of_bytes<CT>(w[e], w[e], 2, 3);
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           *reinterpret_cast<uint4*>(st + (q >> 3) * L::QC + swz(r, (q & 7) + e)) =
-              make_uint4(bf16_of_bytes<CT>(w[2 * e], w[2 * e], 0, 1), bf16_of_bytes<CT>(w[2 * e], w[2 * e], 2, 3),
-                         bf16_of_bytes<CT>(w[2 * e + 1], w[2 * e + 1], 0, 1),
-                         bf16_of_bytes<CT>(w[2 * e + 1], w[2 * e + 1], 2, 3));
+              make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
       }
-      if (!is_k(item)) {
-        float* sc = reinterpret_cast<float*>(sm + L::SC) + (item % NS) * 2 * kKeys + 32 * lw + lane;
+      if (K) {  // its scales, and those of V[t]
+        float* sc = reinterpret_cast<float*>(sm + L::SC) + (((item + 1) / 2) % kScales) * 2 * kKeys + 32 * lw + lane;
         const float2 f = *reinterpret_cast<const float2*>(from + 32 * D + 8 * lane);
         sc[0] = f.x;
         sc[kKeys] = f.y;
@@ -364,7 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           fetch();
           cp_wait<L::RS - 1>();
           begin(item);
-          convert(item);
+          if (is_k(item))
+            convert(item, std::true_type());
+          else
+            convert(item, std::false_type());
           report(item);
         }
       } else {
@@ -396,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     if (warp == 12) {
       // The whole warp walks the loop and one elected lane issues: operands stay in
       // uniform registers (a lane's own branch costs about 40 cycles a product).
-      const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
+      const uint32_t id_s = (1u << 4) | (k8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
       const uint32_t id_pv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
       const uint64_t qd = desc_k(sb + L::Q), kd = desc_k(sb + L::STAGES), vd = desc_mn(sb + L::STAGES, L::QC);
       const int unt = __shfl_sync(0xffffffffu, nt, 0);
@@ -438,17 +481,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
             wait(mFull[vst], vi / NS);
             wait(mFull[ki % NS], ki / NS);
           }
-          wait(mP[w], k);
-          fence_after();
-          if (elect_one()) {
-            const uint64_t bd = vd + vst * (L::SS >> 4);
 #pragma unroll
-            for (int q = 0; q < kKeys / 16; ++q)
-              umma_ts(tb + 256 + D * w, tb + 128 * w + 8 * q, bd + 128 * q, id_pv, (k | q) ? 1u : 0u);
-            if (!both || w == 1) umma_commit(smem_u32(&mEmpty[vst]));
-            if (!more) umma_commit(smem_u32(&mO[w]));
+          for (int u = 0; u < 2; ++u) {  // P V of the tile's halves, as P comes
+            wait(mP[w][u], k);
+            fence_after();
+            if (elect_one()) {
+              const uint64_t bd = vd + vst * (L::SS >> 4);
+#pragma unroll
+              for (int q = 4 * u; q < 4 * u + 4; ++q)
+                umma_ts(tb + 256 + D * w, tb + 128 * w + 8 * q, bd + 128 * q, id_pv, (k | q) ? 1u : 0u);
+              if (u && (!both || w == 1)) umma_commit(smem_u32(&mEmpty[vst]));
+              if (u && !more) umma_commit(smem_u32(&mO[w]));
+            }
+            __syncwarp();
           }
-          __syncwarp();
           if (more) issue_s(w, ki);
         }
       }
@@ -469,81 +515,53 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       alo = seen(a, s, s.pos0 + e / a.G).x;
       ahi = seen(a, s, s.pos0 + f / a.G).y;
     }
-    const float sl2 = a.scale * kLog2e;
-    const bool pos = sl2 > 0.f;
+    const float sl2 = a.scale * kLog2e * (k8 ? qback[two ? 128 * w + row : row] : 1.f);
+    const bool pos = a.scale > 0.f;
     const float mul = pos ? sl2 : 1.f;
     float m = kFloor, l = 0.f;
     const int n = steps(w);
+    const bool idle = !__any_sync(0xffffffffu, live);
     for (int k = 0; k < n; ++k) {
       const int T = tile_at(w, k), tb = t0 + T * kKeys;
       wait(mS[w], k);
       fence_after();
-      uint32_t x[kKeys];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tld32(tS + 32 * q, x + 32 * q);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tld_wait(x + 32 * q);
+      if (idle) {  // no row of this warp is used, whatever its P is
+        if (lane < 2) mbar_arrive(smem_u32(&mP[w][lane]));
+        continue;
+      }
       const int vi = v_item(T);
-      const float* sc = reinterpret_cast<const float*>(sm + L::SC) + (vi % NS) * 2 * kKeys;
+      const float* sc = reinterpret_cast<const float*>(sm + L::SC) + (T % kScales) * 2 * kKeys;
       const bool edge = tb < alo || tb + kKeys > ahi || tb + kKeys > t1;
-      if (k8 || edge) wait(mFull[vi % NS], vi / NS);
-      if (k8) {
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(sc + c);
-          mul2(x + c, f.x, f.y);
-          mul2(x + c + 2, f.z, f.w);
-        }
-      }
-      if (!pos) {  // logits first: the largest product need not be the largest logit
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 2) mul2(x + c, sl2, sl2);
-      }
       const int clo = see.x - tb, chi = min(see.y, t1) - tb;
-      if (edge) {
+      uint32_t x[kKeys];
+      // S of columns [c0, c0 + 64): scales, sign, mask
+      auto logits = [&](int c0) {
+        uint32_t* y = x + c0;
+        if (k8) {
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c)
-          if (c < clo || c >= chi) x[c] = 0xFF800000u;
-        if (CT != kCacheI8 && (tb < alo || tb + kKeys > ahi)) {
-          // values that are not numbers would reach the rows that do not see them
-          bool f = false;
-          const unsigned char* sv = sm + L::STAGES + (vi % NS) * L::SS;
-          for (int e = row; e < L::SS / 16; e += 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(sv + 16 * e);
-            f = f || bf16_not_finite(u.x) || bf16_not_finite(u.y) || bf16_not_finite(u.z) || bf16_not_finite(u.w);
-          }
-          if (f) sbad = 1;
-        }
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < kKeys; c += 2)
-        mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-      const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * mul;
-      const bool move = top > m + kSlack;
-      if (__any_sync(0xffffffffu, move)) {
-        const float f = move ? fast_exp2(m - top) : 1.f;
-        m = move ? top : m;
-        l *= f;
-        if (k > 0) {  // the stream's last P V is done: S came after it
-#pragma unroll 1
-          for (int d = 0; d < D; d += 32) {
-            uint32_t r[32];
-            tld32(tO + d, r);
-            tld_wait(r);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mul2(r + e, f, f);
-            tst32(tO + d, r);
+          for (int c = 0; c < 64; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sc + c0 + c);
+            mul2(y + c, f.x, f.y);
+            mul2(y + c + 2, f.z, f.w);
           }
         }
-      }
-      uint64_t sum[2] = {0, 0};
+        if (!pos) {  // logits first: the largest product need not be the largest logit
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t p[16];
+          for (int c = 0; c < 64; c += 2) mul2(y + c, sl2, sl2);
+        }
+        if (edge) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int c = 32 * q + 2 * e;
+          for (int c = 0; c < 64; ++c)
+            if (c0 + c < clo || c0 + c >= chi) y[c] = 0xFF800000u;
+        }
+      };
+      uint64_t sum[2];
+      uint32_t p[32];
+      // weights of columns [c0, c0 + 64) from their logits
+      auto weights = [&](int c0) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int c = c0 + 2 * e;
           fma2(x + c, mul, -m);
           x[c] = __float_as_uint(fast_exp2(__uint_as_float(x[c])));
           x[c + 1] = __float_as_uint(fast_exp2(__uint_as_float(x[c + 1])));
@@ -552,36 +570,91 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         }
         if (k8) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const int c = 32 * q + 2 * e;
+          for (int e = 0; e < 32; e += 2) {
+            const int c = c0 + 2 * e;
             const float4 f = *reinterpret_cast<const float4*>(sc + kKeys + c);
             mul2(x + c, f.x, f.y);
             mul2(x + c + 2, f.z, f.w);
           }
           if (edge) {  // a masked key's scale need not be a number
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * q + e < clo || 32 * q + e >= chi) x[32 * q + e] = 0;
+            for (int c = c0; c < c0 + 64; ++c)
+              if (c < clo || c >= chi) x[c] = 0;
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            p[e] = bf16_bits2(__uint_as_float(x[32 * q + 2 * e]), __uint_as_float(x[32 * q + 2 * e + 1]));
+          for (int e = 0; e < 32; ++e)
+            p[e] = bf16_bits2(__uint_as_float(x[c0 + 2 * e]), __uint_as_float(x[c0 + 2 * e + 1]));
         }
-        tst16(tS + 16 * q, p);
+      };
+      auto store = [&](int u) {
+        tst32(tS + 32 * u, p);
+        tst_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&mP[w][u]));
+      };
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tld32(tS + 32 * q, x + 32 * q);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tld_wait(x + 32 * q);
+      if (CT != kCacheI8 && (tb < alo || tb + kKeys > ahi)) {
+        // values that are not numbers would reach the rows that do not see them
+        wait(mFull[vi % NS], vi / NS);
+        bool f = false;
+        const unsigned char* sv = sm + L::STAGES + (vi % NS) * L::SS;
+        for (int e = row; e < L::SS / 16; e += 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sv + 16 * e);
+          f = f || bf16_not_finite(u.x) || bf16_not_finite(u.y) || bf16_not_finite(u.z) || bf16_not_finite(u.w);
+        }
+        if (f) sbad = 1;
       }
+      logits(64);
+      float top2 = -INFINITY;
+#pragma unroll
+      for (int c = 64; c < kKeys; c += 2) top2 = max3(top2, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+      for (;;) {
+        // The first half's weights with the maximum so far, next to the tile's own:
+        // the special-function unit need not wait for it.  Where the maximum has to
+        // move they are formed again, from S as it still lies in TMEM.
+        logits(0);
+        float mx[2] = {top2, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 64; c += 2)
+          mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        sum[0] = sum[1] = 0;
+        weights(0);
+        const float top = fmaxf(mx[0], mx[1]) * mul;
+        const bool move = top > m + kSlack;
+        if (!__any_sync(0xffffffffu, move)) break;
+        const float f = move ? fast_exp2(m - top) : 1.f;
+        m = move ? top : m;
+        l *= f;
+        if (k > 0) {  // the stream's last P V is done: S came after it
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            tld32(tO + d, x);
+            tld_wait(x);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) mul2(x + e, f, f);
+            tst32(tO + d, x);
+          }
+        }
+        tld32(tS, x);
+        tld32(tS + 32, x + 32);
+        tld_wait(x);
+        tld_wait(x + 32);
+      }
+      store(0);
+      weights(64);
+      store(1);
       const uint32_t odd[2] = {(uint32_t)sum[1], (uint32_t)(sum[1] >> 32)};
       add2(sum[0], odd);
       l += __uint_as_float((uint32_t)sum[0]) + __uint_as_float((uint32_t)(sum[0] >> 32));
-      tst_wait();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&mP[w]));
     }
     if (n > 0) {
       wait(mO[w], 0);
       fence_after();
     }
-    if (!ok) sfail = 1;
 
     // ---- the rows: joined streams, normalised (or a split's partial) --------------
     float* jo = reinterpret_cast<float*>(sm + L::STAGES);  // [column][row]; every load was used
@@ -652,7 +725,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       for (int r = r0 + warp; r < rt.r1; r += 8)
         redo_row<__nv_bfloat16, CT, D>(a, s, b, h, r, t0, t1, tile, split, parts, r0);
   }
-  if (!ok) sfail = 1;
   fence_before();
   __syncthreads();
   fence_after();
