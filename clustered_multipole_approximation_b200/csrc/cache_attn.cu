@@ -1,5 +1,5 @@
 // Attention of a chunk of new tokens over the paged cache: the choice of a
-// kernel, the division of the keys, the join of the splits, and the fp32 path.
+// kernel, the division of the keys and the join of the splits.
 //
 // Query i of sequence b, at position P = kv_len - new_len + i, sees the keys
 // [lo, hi) of `seen` and takes
@@ -12,30 +12,6 @@
 namespace muse {
 
 namespace {
-
-// fp32 queries, or an fp32 cache: one warp per query row.
-template <typename T, int CT, int D>
-__global__ void __launch_bounds__(128) cache_attn_simt_kernel(const __grid_constant__ CacheAttn a,
-                                                              long long rows) {
-  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (r >= rows) return;
-  const long long bh = r / (a.c.n * a.G);
-  const int pr = (int)(r - bh * (a.c.n * a.G));
-  const int b = (int)(bh / a.c.Hkv), h = (int)(bh - (long long)b * a.c.Hkv);
-  const SeqLen s = seq_len(a.c, b);
-  if (pr >= s.nn * a.G) return;
-  redo_row<T, CT, D>(a, s, b, h, pr, 0, s.kv, 0, 0, 1, 0);
-}
-
-template <typename T, int CT>
-void simt_as(const CacheAttn& a, cudaStream_t st) {
-  const long long rows = (long long)a.B * a.Hq * a.c.n;
-  const unsigned blocks = (unsigned)((rows + 3) / 4);
-  if (a.c.D == 64)
-    cache_attn_simt_kernel<T, CT, 64><<<blocks, 128, 0, st>>>(a, rows);
-  else
-    cache_attn_simt_kernel<T, CT, 128><<<blocks, 128, 0, st>>>(a, rows);
-}
 
 // Joins the splits of one row: W warps take every W-th split each, then the
 // CTA's first warp their sums, always in this order.
@@ -123,9 +99,9 @@ void run_join(const CacheAttn& a, cudaStream_t st) {
     a.S <= 8 ? join_as<T, 128, 1>(a, st) : join_as<T, 128, 8>(a, st);
 }
 
-enum Path { kSimt, kStep, kChunk };
+enum Path { kWide, kStep, kChunk };
 Path path_of(const CacheAttn& a) {
-  if (a.f32 || a.type == kCacheF32) return kSimt;
+  if (a.f32 || a.type == kCacheF32) return kWide;
   return (long long)a.c.n * a.G <= 16 ? kStep : kChunk;
 }
 
@@ -136,18 +112,18 @@ constexpr int kSMs = 148;
 // for).
 Path plan(CacheAttn& a) {
   const Path p = path_of(a);
-  a.RT = a.S = a.minc = 1;
-  a.rows = a.PR = 0;
-  if (p == kSimt) return p;
   const long long cap = (long long)a.c.wide * a.c.page.d;
-  const int size = a.type == kCacheBf16 ? 2 : 1;
   const long long packed = (long long)a.c.n * a.G;
   auto quanta = [](long long x) { return (x + kQuantum - 1) / kQuantum * kQuantum; };
-  if (p == kStep) {
-    a.rows = 16;
-    const long long units = (long long)a.B * a.c.Hkv;
+  a.rows = p == kChunk ? 256 : p == kStep || packed <= 16 ? 16 : 64;
+  a.RT = (int)((packed + a.rows - 1) / a.rows);
+  a.PR = (int)(packed < a.rows ? packed : a.rows);
+  const long long units = (long long)a.B * a.c.Hkv * a.RT;
+  a.S = a.minc = 1;
+  if (p != kChunk) {
     // keys of a split: enough splits for eight CTAs an SM, none of more than
     // 256 KB of cache, and no more than 128 a row
+    const int size = a.type == kCacheF32 ? 4 : a.type == kCacheBf16 ? 2 : 1;
     long long c = quanta(cap * units / (kSMs * 8) + 1);
     const long long most = quanta((256 << 10) / (2 * a.c.D * size));
     if (c > most) c = most;
@@ -158,9 +134,6 @@ Path plan(CacheAttn& a) {
     const long long least = quanta(c * units / (2 * kSMs));
     a.minc = (int)(least < c ? least : c);
   } else {
-    a.rows = 256;
-    a.RT = (int)((packed + 255) / 256);
-    const long long units = (long long)a.B * a.c.Hkv * a.RT;
     // the number of splits whose last wave of CTAs wastes least, each split
     // charged with 3 % for its partials and start
     double best = 1e30;
@@ -174,7 +147,6 @@ Path plan(CacheAttn& a) {
     }
     a.minc = 512;
   }
-  a.PR = (int)(packed < a.rows ? packed : a.rows);
   return p;
 }
 
@@ -195,20 +167,9 @@ size_t cache_attn_workspace(const CacheAttn& a0) {
 void run_cache_attn(const CacheAttn& a0, cudaStream_t st) {
   CacheAttn a = a0;
   const Path p = plan(a);
-  if (p != kSimt) {
-    if (a.S > 1) a.ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(a.ws) + part_bytes(a, false));
-    p == kStep ? run_cache_step(a, st) : run_cache_chunk(a, st);
-    if (a.S > 1) run_join<__nv_bfloat16>(a, st);
-    return;
-  }
-  ProfScope ps(st, "cache_attn");
-  switch (a.type * 2 + a.f32) {
-    case 1: return simt_as<float, kCacheBf16>(a, st);
-    case 2: return simt_as<__nv_bfloat16, kCacheF32>(a, st);
-    case 3: return simt_as<float, kCacheF32>(a, st);
-    case 5: return simt_as<float, kCacheE4m3>(a, st);
-    default: return simt_as<float, kCacheI8>(a, st);
-  }
+  if (a.S > 1) a.ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(a.ws) + part_bytes(a, false));
+  p == kWide ? run_cache_wide(a, st) : p == kStep ? run_cache_step(a, st) : run_cache_chunk(a, st);
+  if (a.S > 1) a.f32 ? run_join<float>(a, st) : run_join<__nv_bfloat16>(a, st);
 }
 
 }  // namespace muse

@@ -206,5 +206,6 @@ __device__ inline bool e4m3_not_finite(uint32_t w) {
 
 void run_cache_step(const CacheAttn& a, cudaStream_t st);  // up to 16 packed rows, bf16 queries
 void run_cache_chunk(const CacheAttn& a, cudaStream_t st);  // more
+void run_cache_wide(const CacheAttn& a, cudaStream_t st);  // fp32 queries or cache
 
 }  // namespace muse
