@@ -1,4 +1,5 @@
-"""Builds libmuse.so (the C-ABI library) in-tree for sm_100a.
+"""Builds libmuse.so (the C-ABI library) in-tree for sm_100a, and _torch_cache.so
+(the paged-cache calls on torch tensors, a CPython module over libmuse.so).
 
     python -m clustered_multipole_approximation_b200.build [--force] [--ptxas-v]
 
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuse.so")
+TORCH_SRC = os.path.join(CSRC, "torch_cache.cpp")
+TORCH_LIB = os.path.join(PKG, "_torch_cache.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -49,8 +52,35 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_torch(force: bool = False) -> str:
+    """The CPython module; libmuse.so has to stand next to it."""
+    header = os.path.join(INCLUDE, "muse.h")
+    if (not force and os.path.exists(TORCH_LIB)
+            and all(os.path.getmtime(p) <= os.path.getmtime(TORCH_LIB) for p in (TORCH_SRC, header, __file__))):
+        return TORCH_LIB
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = TORCH_LIB + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           TORCH_SRC, "-o", tmp, "-L", PKG, "-l:libmuse.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"g++ failed on {TORCH_SRC}:\n{p.stderr}")
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and up_to_date():
+        build_torch()
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -74,6 +104,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError("link failed:\n" + p.stderr)
     os.replace(tmp, LIB)
+    build_torch(force)
     return LIB
 
 

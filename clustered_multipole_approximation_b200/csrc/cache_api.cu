@@ -196,6 +196,7 @@ muse_status muse_attn_cache(const void* Q, const muse_strides* qs, void* O, cons
   if (misaligned(ws, 256)) return fail(MUSE_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
   if (!ws || ws_bytes < cache_attn_workspace(a))
     return fail(MUSE_ERR_WORKSPACE, "workspace too small");
+  if (Q == O) return fail(MUSE_ERR_INVALID_ARG, "O must not share memory with Q");
   a.Q = Q;
   a.O = O;
   a.lse = lse;

@@ -449,10 +449,10 @@ muse_status muse_cache_read(void *K, void *V, const muse_shape *shape, const mus
  * row's range do not reach it, whatever they hold.  Rows i >= new_len[b] of O
  * and lse are left as they were.  Q and O [B,Hq,N,D] (strides qs, os; O's rows
  * must not overlap) share shape->dtype (out_f32 must be 0), lse is [B,Hq,N]
- * fp32 contiguous or NULL.  Logits and sums are fp32; for bf16 queries the
- * softmax weights are rounded once to bf16 for the tensor cores (an int8
- * cache's row scale multiplied in first).  The same call on the same
- * inputs gives the same bits.
+ * fp32 contiguous or NULL; O and lse share no memory with Q.  Logits and sums
+ * are fp32; for bf16 queries the softmax weights are rounded once to bf16 for
+ * the tensor cores (an 8-bit cache's row scale multiplied in first).  The same
+ * call on the same inputs gives the same bits.
  */
 size_t muse_attn_cache_workspace_size(const muse_shape *shape, const muse_cache *cache,
                                       const muse_cache_index *index);
