@@ -177,6 +177,7 @@ struct CacheAttn {
   int S;          // splits a row tile can have
   int minc;       // keys of a split, at least
   int PR;         // rows of a split's partial
+  int cluster;    // the splits of a tile are a cluster and join by themselves
   void* ws;       // partial o, then ml
   float2* ml;
 };

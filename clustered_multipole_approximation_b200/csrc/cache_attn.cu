@@ -102,7 +102,7 @@ void run_join(const CacheAttn& a, cudaStream_t st) {
 enum Path { kWide, kStep, kChunk };
 Path path_of(const CacheAttn& a) {
   if (a.f32 || a.type == kCacheF32) return kWide;
-  return (long long)a.c.n * a.G <= 16 ? kStep : kChunk;
+  return (long long)a.c.n * a.G <= 32 ? kStep : kChunk;
 }
 
 constexpr int kSMs = 148;
@@ -115,11 +115,12 @@ Path plan(CacheAttn& a) {
   const long long cap = (long long)a.c.wide * a.c.page.d;
   const long long packed = (long long)a.c.n * a.G;
   auto quanta = [](long long x) { return (x + kQuantum - 1) / kQuantum * kQuantum; };
-  a.rows = p == kChunk ? 256 : p == kStep || packed <= 16 ? 16 : 64;
+  a.rows = p == kChunk ? 256 : packed <= 16 ? 16 : p == kStep ? 32 : 64;
   a.RT = (int)((packed + a.rows - 1) / a.rows);
   a.PR = (int)(packed < a.rows ? packed : a.rows);
   const long long units = (long long)a.B * a.c.Hkv * a.RT;
   a.S = a.minc = 1;
+  a.cluster = 0;
   if (p != kChunk) {
     // keys of a split: enough splits for eight CTAs an SM, none of more than
     // 256 KB of cache, and no more than 128 a row
@@ -133,6 +134,10 @@ Path plan(CacheAttn& a) {
     // a table far wider than its sequences: shorter splits while few rows fill the SMs
     const long long least = quanta(c * units / (2 * kSMs));
     a.minc = (int)(least < c ? least : c);
+    if (p == kStep && a.S > 1 && a.S <= 16) {  // up to eight join without a second launch
+      a.S = a.S < 8 ? a.S : 8;
+      a.cluster = 1;
+    }
   } else {
     // the number of splits whose last wave of CTAs wastes least, each split
     // charged with 3 % for its partials and start
@@ -161,15 +166,16 @@ size_t part_bytes(const CacheAttn& a, bool ml) {
 size_t cache_attn_workspace(const CacheAttn& a0) {
   CacheAttn a = a0;
   plan(a);
-  return a.S > 1 ? part_bytes(a, false) + part_bytes(a, true) : 256;
+  return a.S > 1 && !a.cluster ? part_bytes(a, false) + part_bytes(a, true) : 256;
 }
 
 void run_cache_attn(const CacheAttn& a0, cudaStream_t st) {
   CacheAttn a = a0;
   const Path p = plan(a);
-  if (a.S > 1) a.ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(a.ws) + part_bytes(a, false));
+  const bool join = a.S > 1 && !a.cluster;
+  if (join) a.ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(a.ws) + part_bytes(a, false));
   p == kWide ? run_cache_wide(a, st) : p == kStep ? run_cache_step(a, st) : run_cache_chunk(a, st);
-  if (a.S > 1) a.f32 ? run_join<float>(a, st) : run_join<__nv_bfloat16>(a, st);
+  if (join) a.f32 ? run_join<float>(a, st) : run_join<__nv_bfloat16>(a, st);
 }
 
 }  // namespace muse

@@ -9,6 +9,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "cache.cuh"
 
 namespace muse {
@@ -204,7 +206,20 @@ __device__ inline bool e4m3_not_finite(uint32_t w) {
   return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
 }
 
-void run_cache_step(const CacheAttn& a, cudaStream_t st);  // up to 16 packed rows, bf16 queries
+// A kernel's leave for more than 48 KB of shared memory, asked for once a device.
+struct LargeShared {
+  std::atomic<uint64_t> done{0};
+  void ensure(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess && dev < 64)
+      done.fetch_or(bit, std::memory_order_release);
+  }
+};
+
+void run_cache_step(const CacheAttn& a, cudaStream_t st);  // up to 32 packed rows, bf16 queries
 void run_cache_chunk(const CacheAttn& a, cudaStream_t st);  // more
 void run_cache_wide(const CacheAttn& a, cudaStream_t st);  // fp32 queries or cache
 

@@ -736,7 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
 template <int CT, int D>
 void launch(const CacheAttn& a, cudaStream_t st) {
   const int smem = ChunkL<CT, D>::TOTAL;
-  cudaFuncSetAttribute(cache_chunk_kernel<CT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static LargeShared allowed;
+  allowed.ensure((const void*)cache_chunk_kernel<CT, D>, smem);
   const long long blocks = (long long)a.B * a.c.Hkv * a.RT * a.S;
   cache_chunk_kernel<CT, D><<<(unsigned)blocks, kThreads, smem, st>>>(a);
 }

@@ -1,4 +1,4 @@
-// Attention of single tokens (and of a few: up to 16 packed rows a kv-head)
+// Attention of single tokens (and of a few: up to 32 packed rows a kv-head)
 // over the paged cache, bf16 queries.
 //
 // One CTA of four warps takes a split of one (sequence, kv-head)'s keys.  The
@@ -6,17 +6,23 @@
 // through a ring of shared memory (cp.async, several blocks in flight, no
 // block-wide barrier in the loop) and keeps its own online softmax, so that
 // warps drift apart and loads never stop; they join once, at the end, in a
-// fixed order.  Products run on mma.sync m16n8k16: with at most 16 rows a
-// tile of the fifth-generation tensor cores would be seven-eighths padding,
+// fixed order.  Products run on mma.sync m16n8k16: with at most 32 rows a
+// tile of the fifth-generation tensor cores would be three quarters padding,
 // and its results would take the way over TMEM.
 //   S = Q K^T     K rows as the B operand.  The contraction's order is free,
 //                 so an 8-bit row is read 16 bytes a lane and Q's columns are
-//                 permuted to match; converted in registers.
+//                 permuted to match; converted in registers to fp16 (half the
+//                 instructions of bf16), Q's rows brought into fp16's range by
+//                 powers of two.
 //   o += P V      V as the B operand: ldmatrix.trans (bf16), or pairs of bytes
 //                 from neighbouring keys' rows (8-bit) with the output columns
 //                 permuted to match.
 // Scales of 8-bit rows multiply S's columns and P's columns (before its one
-// rounding to bf16).
+// rounding to bf16).  Up to eight splits are one thread-block cluster and join
+// through its distributed shared memory (one launch, no workspace traffic);
+// more leave partials for cache_join_kernel.
+#include <cooperative_groups.h>
+
 #include "cache_attn.cuh"
 #include "kernels.h"
 #include "mma_sync.cuh"
@@ -27,7 +33,7 @@ namespace {
 
 constexpr int kWarps = 4;
 
-template <int CT, int D>
+template <int CT, int D, int MT>
 struct StepL {
   static constexpr int SZ = CT == kCacheBf16 ? 2 : 1;
   static constexpr int KB = SZ * D > 128 ? 16 : 32;  // keys of a block
@@ -38,9 +44,11 @@ struct StepL {
   static constexpr int STAGE = 2 * HALF + SCALES;
   static constexpr int NS = 3;
   static constexpr int RING = NS * STAGE;
-  static constexpr int JOIN = 16 * D * 4 + 16 * 8;  // o, (m, l) of a warp
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int JOIN = ROWS * D * 4 + ROWS * 8;  // o, (m, l) of a warp
   static constexpr int WARP = RING > JOIN ? RING : JOIN;
-  static constexpr int TOTAL = kWarps * WARP;
+  static constexpr int Q = kWarps * WARP, QP = 2 * D + 16;  // query rows, padded against bank conflicts
+  static constexpr int TOTAL = Q + ROWS * QP;
 };
 
 // Byte offset of 16-byte piece c of key row r.  Each pattern keeps the lanes
@@ -55,22 +63,33 @@ __device__ inline int at16(int r, int c) {
   return slot * 64 + ((c ^ (((r >> 2) & 1) << 1)) << 4);
 }
 
-template <int CT, int D>
+// Column of query element d: for an 8-bit cache the order in which a lane's 16
+// bytes of a K row meet the k = 16 steps.
+template <bool k8>
+__device__ inline int q_column(int d) {
+  if (!k8) return d;
+  const int t = (d >> 4) & 3, k = (d >> 2) & 3, e = d & 3;
+  return (d & 64) + 16 * k + 2 * t + (e & 1) + 8 * (e >> 1);
+}
+
+template <int CT, int D, int MT, bool CL>
 __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_constant__ CacheAttn a) {
-  using L = StepL<CT, D>;
+  using L = StepL<CT, D, MT>;
   constexpr int KB = L::KB, NT = KB / 8, DT = D / 8;
+  constexpr bool k8 = L::SZ == 1;
   extern __shared__ __align__(128) unsigned char step_sm[];
+  __shared__ float qback[L::ROWS];  // 8-bit: the power of two that undoes a row's factor
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const long long tile = blockIdx.x / a.S;
   const int split = (int)(blockIdx.x - tile * a.S);
   const int b = (int)(tile / a.c.Hkv), h = (int)(tile - (long long)b * a.c.Hkv);
   const SeqLen s = seq_len(a.c, b);
   if (s.nn == 0) return;
-  const RowTile rt = row_tile(a, s, 0, 16);
+  const RowTile rt = row_tile(a, s, 0, L::ROWS);
   const int len = rt.hi - rt.lo, parts = split_count(a, len);
-  if (split >= parts) return;
+  if (split >= parts && (!CL || parts == 1)) return;
   const int keys = split_keys(a, len);
-  const int t0 = rt.lo + split * keys, t1 = min(rt.hi, t0 + keys);
+  const int t0 = min(rt.hi, rt.lo + split * keys), t1 = min(rt.hi, t0 + keys);
   unsigned char* ring = step_sm + warp * L::WARP;
 
   // this warp's blocks: warp, warp + 4, ... of the split's
@@ -112,31 +131,62 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
     row = next;
   }
 
-  // Q fragments (rows g and g + 8, zero past the tile)
-  uint32_t q[D / 16][4];
-  {
-    const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
-    const bool lg = g < rt.r1, lh = g + 8 < rt.r1;
-    const __nv_bfloat16* qg = Q + (lg ? row_at(a, b, h, g).q : 0);
-    const __nv_bfloat16* qh = Q + (lh ? row_at(a, b, h, g + 8).q : 0);
+  // the query rows (zero past the tile), four threads a row
+  for (int r = tid >> 2; r < L::ROWS; r += 8 * kWarps) {
+    const bool live = r < rt.r1;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.Q) + (live ? row_at(a, b, h, r).q : 0);
+    unsigned char* dst = step_sm + L::Q + r * L::QP;
+    uint4 v[D / 32];
+    float top = 0.f;
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      // columns of the first and second half of the fragment's k = 16
-      const int c0 = L::SZ == 2 ? 16 * k + 2 * t4 : (k >> 2) * 64 + 16 * t4 + 4 * (k & 3);
-      const int c1 = c0 + (L::SZ == 2 ? 8 : 2);
-      q[k][0] = lg ? *reinterpret_cast<const uint32_t*>(qg + c0) : 0;
-      q[k][1] = lh ? *reinterpret_cast<const uint32_t*>(qh + c0) : 0;
-      q[k][2] = lg ? *reinterpret_cast<const uint32_t*>(qg + c1) : 0;
-      q[k][3] = lh ? *reinterpret_cast<const uint32_t*>(qh + c1) : 0;
+    for (int c = 0; c < D / 32; ++c) {  // columns 8 t4 + 32 c ..
+      v[c] = live ? *reinterpret_cast<const uint4*>(src + 8 * t4 + 32 * c) : make_uint4(0, 0, 0, 0);
+      if (!k8) {
+        *reinterpret_cast<uint4*>(dst + 16 * t4 + 64 * c) = v[c];
+      } else {
+        float x[8];
+        load8_in(reinterpret_cast<const __nv_bfloat16*>(&v[c]), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+      }
+    }
+    if (k8) {
+      // a maximum in [2^14, 2^15): exact for values down to 2^-31 of it
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float2 f = half_factor(top);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float x[8];
+        load8_in(reinterpret_cast<const __nv_bfloat16*>(&v[c]), x);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2)
+          *reinterpret_cast<uint32_t*>(dst + 2 * q_column<k8>(8 * t4 + 32 * c + e)) = pack_h2(x[e] * f.x, x[e + 1] * f.x);
+      }
+      if (t4 == 0) qback[r] = f.y;
     }
   }
-  const int2 sg = seen(a, s, s.pos0 + g / a.G), sh = seen(a, s, s.pos0 + (g + 8) / a.G);
-  const float sl2 = a.scale * kLog2e;
-
-  float o[DT][4];
+  __syncthreads();
+  int2 see[MT][2];   // of rows 16 i + g and 16 i + g + 8
+  float mul[MT][2];  // their product to base-2 logit
 #pragma unroll
-  for (int j = 0; j < DT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  float m0 = kFloor, m1 = kFloor, l0 = 0.f, l1 = 0.f;  // l: this lane's share
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 16 * i + 8 * e + g;
+      see[i][e] = seen(a, s, s.pos0 + r / a.G);
+      see[i][e].y = min(see[i][e].y, t1);
+      mul[i][e] = a.scale * kLog2e * (k8 ? qback[r] : 1.f);
+    }
+
+  float o[MT][DT][4], m[MT][2], l[MT][2];  // l: this lane's share
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    m[i][0] = m[i][1] = kFloor;
+    l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < DT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+  }
   bool bad = false;
 
   for (int i = 0; i < mine; ++i) {
@@ -151,50 +201,66 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
     const unsigned char* sv = sk + L::HALF;
     const float* sc = reinterpret_cast<const float*>(sk + 2 * L::HALF);
     const int tb = key0(i);
-    float x[NT][4];
+    float x[MT][NT][4] = {};
+    // two (bf16) or four (8-bit) k = 16 steps at a time
+    constexpr int KS = k8 ? 4 : 2;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
-      if (L::SZ == 2) {
+    for (int c = 0; c < D / (16 * KS); ++c) {
+      uint32_t q[MT][KS][4];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+      for (int u = 0; u < MT; ++u)
+#pragma unroll
+        for (int e = 0; e < KS; ++e)
+          ldsm_x4(smem_u32(step_sm + L::Q + (16 * u + (lane & 15)) * L::QP + 32 * (KS * c + e) + 16 * (lane >> 4)),
+                  q[u][e][0], q[u][e][1], q[u][e][2], q[u][e][3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (!k8) {
           uint32_t r0, r1, r2, r3;
           ldsm_x4(smem_u32(sk + at16<CT, D, false>(8 * n + (lane & 7), 4 * c + (lane >> 3))), r0, r1, r2, r3);
-          mma_bf16(x[n], q[2 * c], r0, r1);
-          mma_bf16(x[n], q[2 * c + 1], r2, r3);
-        }
-      } else {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
+          for (int u = 0; u < MT; ++u) {
+            mma_bf16(x[u][n], q[u][0], r0, r1);
+            mma_bf16(x[u][n], q[u][KS / 2], r2, r3);
+          }
+        } else {
           const uint4 w = *reinterpret_cast<const uint4*>(sk + at16<CT, D, false>(8 * n + g, 4 * c + t4));
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mma_bf16(x[n], q[4 * c + e], bf16_of_bytes<CT>(ww[e], ww[e], 0, 1),
-                     bf16_of_bytes<CT>(ww[e], ww[e], 2, 3));
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t b0 = half_of_bytes<CT>(ww[e], 0), b1 = half_of_bytes<CT>(ww[e], 2);
+#pragma unroll
+            for (int u = 0; u < MT; ++u) mma_f16(x[u][n], q[u][e % KS], b0, b1);
+          }
         }
       }
     }
     // logits in base 2, columns 8 n + 2 t4 + {0, 1}
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float2 ks = make_float2(sl2, sl2);
-      if (L::SZ == 1) {
-        const float2 f = *reinterpret_cast<const float2*>(sc + 8 * n + 2 * t4);
-        x[n][0] *= f.x, x[n][1] *= f.y, x[n][2] *= f.x, x[n][3] *= f.y;
-      }
-      x[n][0] *= ks.x, x[n][1] *= ks.y, x[n][2] *= ks.x, x[n][3] *= ks.y;
-    }
-    const bool edge = tb < rt.alo || tb + KB > rt.ahi || tb + KB > t1;
-    if (edge) {  // the same in the whole warp
+      float2 f = make_float2(1.f, 1.f);
+      if (k8) f = *reinterpret_cast<const float2*>(sc + 8 * n + 2 * t4);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int u = 0; u < MT; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int t = tb + 8 * n + 2 * t4 + (e & 1);
-          const int2 ks = e < 2 ? sg : sh;
-          if (t < ks.x || t >= ks.y || t >= t1) x[n][e] = -INFINITY;
+          if (k8) x[u][n][e] *= e & 1 ? f.y : f.x;
+          x[u][n][e] *= mul[u][e >> 1];
         }
+    }
+    const bool edge = tb < rt.alo || tb + KB > rt.ahi || tb + KB > t1;
+    auto masked = [&](int u, int n, int e) {
+      const int t = tb + 8 * n + 2 * t4 + (e & 1);
+      return t < see[u][e >> 1].x || t >= see[u][e >> 1].y;
+    };
+    if (edge) {  // the same in the whole warp
+#pragma unroll
+      for (int u = 0; u < MT; ++u)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (masked(u, n, e)) x[u][n][e] = -INFINITY;
       if (CT != kCacheI8 && (tb < rt.alo || tb + KB > rt.ahi)) {
         bool f = false;
         for (int e = lane; e < L::HALF / 4; e += 32) {
@@ -204,65 +270,70 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
         bad = bad || __any_sync(0xffffffffu, f);
       }
     }
-    float n0 = -INFINITY, n1 = -INFINITY;
+    float top[MT][2];
+    bool moves = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      n0 = fmaxf(n0, fmaxf(x[n][0], x[n][1]));
-      n1 = fmaxf(n1, fmaxf(x[n][2], x[n][3]));
-    }
+    for (int u = 0; u < MT; ++u)
 #pragma unroll
-    for (int w = 1; w < 4; w <<= 1) {
-      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, w));
-      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, w));
-    }
-    const bool v0 = n0 > m0 + kSlack, v1 = n1 > m1 + kSlack;
-    if (__any_sync(0xffffffffu, v0 || v1)) {
-      const float f0 = v0 ? fast_exp2(m0 - n0) : 1.f, f1 = v1 ? fast_exp2(m1 - n1) : 1.f;
-      m0 = v0 ? n0 : m0;
-      m1 = v1 ? n1 : m1;
-      l0 *= f0;
-      l1 *= f1;
+      for (int e = 0; e < 2; ++e) {
+        float y = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < DT; ++j) o[j][0] *= f0, o[j][1] *= f0, o[j][2] *= f1, o[j][3] *= f1;
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      x[n][0] = fast_exp2(x[n][0] - m0);
-      x[n][1] = fast_exp2(x[n][1] - m0);
-      x[n][2] = fast_exp2(x[n][2] - m1);
-      x[n][3] = fast_exp2(x[n][3] - m1);
-      l0 += x[n][0] + x[n][1];
-      l1 += x[n][2] + x[n][3];
-    }
-    if (L::SZ == 1) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float2 f = *reinterpret_cast<const float2*>(sc + KB + 8 * n + 2 * t4);
-        x[n][0] *= f.x, x[n][1] *= f.y, x[n][2] *= f.x, x[n][3] *= f.y;
+        for (int n = 0; n < NT; ++n) y = fmaxf(y, fmaxf(x[u][n][2 * e], x[u][n][2 * e + 1]));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+        top[u][e] = y;
+        moves = moves || y > m[u][e] + kSlack;
       }
-      if (edge) {  // a masked key's scale need not be a number
+    if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int u = 0; u < MT; ++u) {
+        float f[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = tb + 8 * n + 2 * t4 + (e & 1);
-            const int2 ks = e < 2 ? sg : sh;
-            if (t < ks.x || t >= ks.y || t >= t1) x[n][e] = 0.f;
-          }
+        for (int e = 0; e < 2; ++e) {
+          const bool v = top[u][e] > m[u][e] + kSlack;
+          f[e] = v ? fast_exp2(m[u][e] - top[u][e]) : 1.f;
+          m[u][e] = v ? top[u][e] : m[u][e];
+          l[u][e] *= f[e];
+        }
+#pragma unroll
+        for (int j = 0; j < DT; ++j) o[u][j][0] *= f[0], o[u][j][1] *= f[0], o[u][j][2] *= f[1], o[u][j][3] *= f[1];
       }
     }
 #pragma unroll
-    for (int u = 0; u < KB / 16; ++u) {
-      const uint32_t p[4] = {bf16_bits2(x[2 * u][0], x[2 * u][1]), bf16_bits2(x[2 * u][2], x[2 * u][3]),
-                             bf16_bits2(x[2 * u + 1][0], x[2 * u + 1][1]),
-                             bf16_bits2(x[2 * u + 1][2], x[2 * u + 1][3])};
-      if (L::SZ == 2) {
+    for (int n = 0; n < NT; ++n) {
+      float2 f = make_float2(1.f, 1.f);
+      if (k8) f = *reinterpret_cast<const float2*>(sc + KB + 8 * n + 2 * t4);
+#pragma unroll
+      for (int u = 0; u < MT; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = fast_exp2(x[u][n][e] - m[u][e >> 1]);
+          l[u][e >> 1] += y;
+          x[u][n][e] = k8 ? y * (e & 1 ? f.y : f.x) : y;
+          // a masked key's scale need not be a number
+          if (k8 && edge && masked(u, n, e)) x[u][n][e] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < KB / 16; ++k) {
+      uint32_t p[MT][4];
+#pragma unroll
+      for (int u = 0; u < MT; ++u) {
+        p[u][0] = bf16_bits2(x[u][2 * k][0], x[u][2 * k][1]);
+        p[u][1] = bf16_bits2(x[u][2 * k][2], x[u][2 * k][3]);
+        p[u][2] = bf16_bits2(x[u][2 * k + 1][0], x[u][2 * k + 1][1]);
+        p[u][3] = bf16_bits2(x[u][2 * k + 1][2], x[u][2 * k + 1][3]);
+      }
+      if (!k8) {
 #pragma unroll
         for (int j = 0; j < DT; j += 2) {
           uint32_t r0, r1, r2, r3;
-          ldsm_x4_t(smem_u32(sv + at16<CT, D, true>(16 * u + (lane & 15), j + (lane >> 4))), r0, r1, r2, r3);
-          mma_bf16(o[j], p, r0, r1);
-          mma_bf16(o[j + 1], p, r2, r3);
+          ldsm_x4_t(smem_u32(sv + at16<CT, D, true>(16 * k + (lane & 15), j + (lane >> 4))), r0, r1, r2, r3);
+#pragma unroll
+          for (int u = 0; u < MT; ++u) {
+            mma_bf16(o[u][j], p[u], r0, r1);
+            mma_bf16(o[u][j + 1], p[u], r2, r3);
+          }
         }
       } else {
         // keys 2 t4, + 1, + 8, + 9 of the 16; output column D / 8 g + j
@@ -270,7 +341,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
         uint32_t v[4][W];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 16 * u + 2 * t4 + (e & 1) + 8 * (e >> 1);
+          const int r = 16 * k + 2 * t4 + (e & 1) + 8 * (e >> 1);
           if (D == 128) {
             const uint4 w = *reinterpret_cast<const uint4*>(sv + at16<CT, D, true>(r, g));
             v[e][0] = w.x, v[e][1] = w.y, v[e][W - 2] = w.z, v[e][W - 1] = w.w;
@@ -280,9 +351,12 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
           }
         }
 #pragma unroll
-        for (int j = 0; j < DT; ++j)
-          mma_bf16(o[j], p, bf16_of_bytes<CT>(v[0][j >> 2], v[1][j >> 2], j & 3, j & 3),
-                   bf16_of_bytes<CT>(v[2][j >> 2], v[3][j >> 2], j & 3, j & 3));
+        for (int j = 0; j < DT; ++j) {
+          const uint32_t b0 = bf16_of_bytes<CT>(v[0][j >> 2], v[1][j >> 2], j & 3, j & 3);
+          const uint32_t b1 = bf16_of_bytes<CT>(v[2][j >> 2], v[3][j >> 2], j & 3, j & 3);
+#pragma unroll
+          for (int u = 0; u < MT; ++u) mma_bf16(o[u][j], p[u], b0, b1);
+        }
       }
     }
     __syncwarp();  // the block is read: its stage is loaded next
@@ -290,70 +364,124 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
   cp_wait<0>();
 
   // ---- join the warps --------------------------------------------------------
-#pragma unroll
-  for (int w = 1; w < 4; w <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, w);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, w);
-  }
   __syncwarp();
   {
     float* jo = reinterpret_cast<float*>(ring);
-    float2* jm = reinterpret_cast<float2*>(jo + 16 * D);
+    float2* jm = reinterpret_cast<float2*>(jo + L::ROWS * D);
 #pragma unroll
-    for (int j = 0; j < DT; ++j)
+    for (int u = 0; u < MT; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int n = 2 * t4 + (e & 1);
-        const int d = L::SZ == 2 ? 8 * j + n : DT * n + j;
-        jo[(g + 8 * (e >> 1)) * D + d] = o[j][e];
+      for (int e = 0; e < 2; ++e) {
+        l[u][e] += __shfl_xor_sync(0xffffffffu, l[u][e], 1);
+        l[u][e] += __shfl_xor_sync(0xffffffffu, l[u][e], 2);
+        const int r = 16 * u + 8 * e + g;
+#pragma unroll
+        for (int j = 0; j < DT; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int n = 2 * t4 + c;
+            jo[r * D + (k8 ? DT * n + j : 8 * j + n)] = o[u][j][2 * e + c];
+          }
+        if (t4 == 0) jm[r] = make_float2(m[u][e], l[u][e]);
       }
-    if (t4 == 0) {
-      jm[g] = make_float2(m0, l0);
-      jm[g + 8] = make_float2(m1, l1);
-    }
   }
-  if (__syncthreads_or(bad)) {
-    for (int r = warp; r < rt.r1; r += kWarps)
-      redo_row<__nv_bfloat16, CT, D>(a, s, b, h, r, t0, t1, tile, split, parts, 0);
-    return;
-  }
-  for (int e = tid; e < rt.r1 * (D / 8); e += 32 * kWarps) {
-    const int r = e / (D / 8), c = e % (D / 8);
-    float2 ml[kWarps];
-    float m = kFloor, l = 0.f, y[8] = {};
+  // The CTA's o, m, l of columns [8 c, 8 c + 8) of row r: the result, a partial
+  // in the workspace, or one for the cluster (in place of the first warp's).
+  float* co = reinterpret_cast<float*>(step_sm);
+  __shared__ float2 cml[L::ROWS];
+  auto finish = [&](int r, int c, float (&y)[8], float mr, float lr) {
+    const float inv = lr == 0.f ? 0.f : 1.f / lr;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      ml[w] = reinterpret_cast<const float2*>(step_sm + w * L::WARP + 16 * D * 4)[r];
-      m = fmaxf(m, ml[w].x);
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = fast_exp2(ml[w].x - m);
-      l += ml[w].y * f;
-      const float* jo = reinterpret_cast<const float*>(step_sm + w * L::WARP) + r * D + 8 * c;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) y[u] = fmaf(jo[u], f, y[u]);
-    }
-    if (parts > 1) {
-      store8(part_o<D>(a, tile, split, r) + 8 * c, y);
-      if (c == 0) *part_ml(a, tile, split, r) = make_float2(m, l);
-      continue;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) y[u] *= inv;
+    for (int e = 0; e < 8; ++e) y[e] *= inv;
     const RowAt at = row_at(a, b, h, r);
     store8(static_cast<__nv_bfloat16*>(a.O) + at.o + 8 * c, y);
-    if (a.lse && c == 0) a.lse[at.lse] = lse_of(m, l);
+    if (a.lse && c == 0) a.lse[at.lse] = lse_of(mr, lr);
+  };
+  auto emit = [&](int r, int c, float (&y)[8], float mr, float lr) {
+    if (parts == 1) return finish(r, c, y, mr, lr);
+    if (CL) {
+      store8(co + r * D + 8 * c, y);
+      if (c == 0) cml[r] = make_float2(mr, lr);
+    } else {
+      store8(part_o<D>(a, tile, split, r) + 8 * c, y);
+      if (c == 0) *part_ml(a, tile, split, r) = make_float2(mr, lr);
+    }
+  };
+  if (__syncthreads_or(bad)) {
+    for (int r = warp; r < rt.r1; r += kWarps) {
+      float y[8], mr, lr;
+      row_over_keys<__nv_bfloat16, CT, D>(a, s, b, h, r, t0, t1, y, mr, lr);
+      if (lane < D / 8) emit(r, lane, y, lr == 0.f ? kFloor : mr, lr);
+    }
+  } else {
+    for (int e = tid; e < rt.r1 * (D / 8); e += 32 * kWarps) {
+      const int r = e / (D / 8), c = e % (D / 8);
+      float2 ml[kWarps];
+      float mr = kFloor, lr = 0.f, y[8] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        ml[w] = reinterpret_cast<const float2*>(step_sm + w * L::WARP + L::ROWS * D * 4)[r];
+        mr = fmaxf(mr, ml[w].x);
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = fast_exp2(ml[w].x - mr);
+        lr += ml[w].y * f;
+        const float* jo = reinterpret_cast<const float*>(step_sm + w * L::WARP) + r * D + 8 * c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(jo[i], f, y[i]);
+      }
+      emit(r, c, y, mr, lr);
+    }
   }
+  if (!CL || parts == 1) return;
+
+  // ---- join the cluster's splits, every CTA a share of the columns -------------
+  auto cluster = cooperative_groups::this_cluster();
+  cluster.sync();
+  for (int e = split * 32 * kWarps + tid; e < rt.r1 * (D / 8); e += a.S * 32 * kWarps) {
+    const int r = e / (D / 8), c = e % (D / 8);
+    float mr = kFloor, lr = 0.f, y[8] = {};
+    for (int p = 0; p < parts; ++p) mr = fmaxf(mr, cluster.map_shared_rank(cml, p)[r].x);
+    for (int p = 0; p < parts; ++p) {
+      const float2 ml = cluster.map_shared_rank(cml, p)[r];
+      const float f = fast_exp2(ml.x - mr);
+      lr += ml.y * f;
+      float z[8];
+      load8_in(cluster.map_shared_rank(co, p) + r * D + 8 * c, z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(z[i], f, y[i]);
+    }
+    finish(r, c, y, mr, lr);
+  }
+  cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-template <int CT, int D>
+template <int CT, int D, int MT, bool CL>
 void launch(const CacheAttn& a, cudaStream_t st) {
-  const int smem = StepL<CT, D>::TOTAL;
-  cudaFuncSetAttribute(cache_step_kernel<CT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  const long long blocks = (long long)a.B * a.c.Hkv * a.S;
-  cache_step_kernel<CT, D><<<(unsigned)blocks, 32 * kWarps, smem, st>>>(a);
+  const int smem = StepL<CT, D, MT>::TOTAL;
+  auto* kernel = cache_step_kernel<CT, D, MT, CL>;
+  static LargeShared allowed;
+  allowed.ensure((const void*)kernel, smem);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((long long)a.B * a.c.Hkv * a.S));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CL ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, kernel, a);
+}
+template <int CT, int D>
+void launch_as(const CacheAttn& a, cudaStream_t st) {
+  if (a.rows == 16)
+    a.cluster ? launch<CT, D, 1, true>(a, st) : launch<CT, D, 1, false>(a, st);
+  else
+    a.cluster ? launch<CT, D, 2, true>(a, st) : launch<CT, D, 2, false>(a, st);
 }
 
 }  // namespace
@@ -361,12 +489,12 @@ void launch(const CacheAttn& a, cudaStream_t st) {
 void run_cache_step(const CacheAttn& a, cudaStream_t st) {
   ProfScope ps(st, "cache_step");
   switch (a.type * 2 + (a.c.D == 128)) {
-    case 2 * kCacheBf16: return launch<kCacheBf16, 64>(a, st);
-    case 2 * kCacheBf16 + 1: return launch<kCacheBf16, 128>(a, st);
-    case 2 * kCacheE4m3: return launch<kCacheE4m3, 64>(a, st);
-    case 2 * kCacheE4m3 + 1: return launch<kCacheE4m3, 128>(a, st);
-    case 2 * kCacheI8: return launch<kCacheI8, 64>(a, st);
-    default: return launch<kCacheI8, 128>(a, st);
+    case 2 * kCacheBf16: return launch_as<kCacheBf16, 64>(a, st);
+    case 2 * kCacheBf16 + 1: return launch_as<kCacheBf16, 128>(a, st);
+    case 2 * kCacheE4m3: return launch_as<kCacheE4m3, 64>(a, st);
+    case 2 * kCacheE4m3 + 1: return launch_as<kCacheE4m3, 128>(a, st);
+    case 2 * kCacheI8: return launch_as<kCacheI8, 64>(a, st);
+    default: return launch_as<kCacheI8, 128>(a, st);
   }
 }
 

@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(256) cache_wide_kernel(const __grid_constant__
 template <typename T, int CT, int D, int R>
 void launch(const CacheAttn& a, cudaStream_t st) {
   const int smem = WideL<D, R>::TOTAL;
-  cudaFuncSetAttribute(cache_wide_kernel<T, CT, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static LargeShared allowed;
+  allowed.ensure((const void*)cache_wide_kernel<T, CT, D, R>, smem);
   const long long blocks = (long long)a.B * a.c.Hkv * a.RT * a.S;
   cache_wide_kernel<T, CT, D, R><<<(unsigned)blocks, 256, smem, st>>>(a);
 }
