@@ -115,7 +115,7 @@ Path plan(CacheAttn& a) {
   const long long cap = (long long)a.c.wide * a.c.page.d;
   const long long packed = (long long)a.c.n * a.G;
   auto quanta = [](long long x) { return (x + kQuantum - 1) / kQuantum * kQuantum; };
-  a.rows = p == kChunk ? 256 : packed <= 16 ? 16 : p == kStep ? 32 : 64;
+  a.rows = p == kChunk ? 256 : p == kStep && packed <= 8 ? 8 : packed <= 16 ? 16 : p == kStep ? 32 : 64;
   a.RT = (int)((packed + a.rows - 1) / a.rows);
   a.PR = (int)(packed < a.rows ? packed : a.rows);
   const long long units = (long long)a.B * a.c.Hkv * a.RT;
@@ -123,10 +123,10 @@ Path plan(CacheAttn& a) {
   a.cluster = 0;
   if (p != kChunk) {
     // keys of a split: enough splits for eight CTAs an SM, none of more than
-    // 256 KB of cache, and no more than 128 a row
+    // 512 KB of cache, and no more than 128 a row
     const int size = a.type == kCacheF32 ? 4 : a.type == kCacheBf16 ? 2 : 1;
     long long c = quanta(cap * units / (kSMs * 8) + 1);
-    const long long most = quanta((256 << 10) / (2 * a.c.D * size));
+    const long long most = quanta((512 << 10) / (2 * a.c.D * size));
     if (c > most) c = most;
     if (c * 128 < cap) c = quanta((cap + 127) / 128);
     a.S = (int)((cap + c - 1) / c);

@@ -158,35 +158,62 @@ __device__ __noinline__ void redo_row(const CacheAttn& a, const SeqLen& s, int b
   if (a.lse && lane == 0) a.lse[at.lse] = lse_of(m, l);
 }
 
-// Two 8-bit values as a bf16 pair, exact: byte i of x and byte j of y.
-//   e4m3  through the hardware conversion (NaN stays NaN), whose halves are
-//         bf16 values, so that the upper halves of the fp32 forms are it;
-//   int8  q = (128 + (q & 127)) - (128 + (q & 128)), both terms bf16 values
-//         made by OR with the bits of 128.
-template <int CT>
-__device__ inline uint32_t bf16_of_bytes(uint32_t x, uint32_t y, int i, int j) {
-  if (CT == kCacheE4m3) {
-    const float2 f = e4m3x2(__byte_perm(x, y, i | ((4 + j) << 4)));
-    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-  }
-  const uint32_t w = __byte_perm(x, y, i | ((4 + j) << 8));
+// e4m3 pairs in the low (high) half of x as fp16, exact.
+__device__ inline uint32_t half_of_e4m3_lo(uint32_t x) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ inline uint32_t half_of_e4m3_hi(uint32_t x) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}\n" : "=r"(y) : "r"(x));
+  return y;
+}
+// An fp16 pair of bf16 values as bf16: the upper halves of the fp32 forms.
+__device__ inline uint32_t bf16_of_half(uint32_t x) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+}
+// int8 pair in bytes 0 and 2 of w as bf16, exact: q = (128 + (q & 127)) -
+// (128 + (q & 128)), both terms bf16 values made by OR with the bits of 128.
+__device__ inline uint32_t bf16_of_i8(uint32_t w) {
   const uint32_t p = (w & 0x007F007Fu) | 0x43004300u, n = (w & 0x00800080u) | 0x43004300u;
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&p),
                                    *reinterpret_cast<const __nv_bfloat162*>(&n));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-
-// The same as an fp16 pair, bytes i and i + 1 of x: e4m3 by the hardware
-// conversion, int8 from the bits of 1024 + 128 + q.
+// Byte i of x and of y, i = 0 .. 3, as four bf16 pairs.
 template <int CT>
-__device__ inline uint32_t half_of_bytes(uint32_t x, int i) {
+__device__ inline void bf16_pairs(uint32_t x, uint32_t y, uint32_t (&o)[4]) {
   if (CT == kCacheE4m3) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> (8 * i)), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    const uint32_t a = __byte_perm(x, y, 0x5140), b = __byte_perm(x, y, 0x7362);
+    o[0] = bf16_of_half(half_of_e4m3_lo(a));
+    o[1] = bf16_of_half(half_of_e4m3_hi(a));
+    o[2] = bf16_of_half(half_of_e4m3_lo(b));
+    o[3] = bf16_of_half(half_of_e4m3_hi(b));
+  } else {
+    o[0] = bf16_of_i8(__byte_perm(x, y, 0x0400));
+    o[1] = bf16_of_i8(__byte_perm(x, y, 0x0501));
+    o[2] = bf16_of_i8(__byte_perm(x, y, 0x0602));
+    o[3] = bf16_of_i8(__byte_perm(x, y, 0x0703));
   }
-  const uint32_t w = __byte_perm(x ^ 0x80808080u, 0x64646464u, i | 0x40 | ((i + 1) << 8) | 0x4000);
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&w), __floats2half2_rn(1152.f, 1152.f));
-  return *reinterpret_cast<const uint32_t*>(&d);
+}
+// Bytes (0, 1) and (2, 3) of x as bf16 pairs, and as fp16 pairs (int8 from the
+// bits of 1024 + 128 + q).
+template <int CT>
+__device__ inline uint2 bf16_of_word(uint32_t x) {
+  if (CT == kCacheE4m3) return make_uint2(bf16_of_half(half_of_e4m3_lo(x)), bf16_of_half(half_of_e4m3_hi(x)));
+  return make_uint2(bf16_of_i8(__byte_perm(x, x, 0x0100)), bf16_of_i8(__byte_perm(x, x, 0x0302)));
+}
+template <int CT>
+__device__ inline uint2 half_of_word(uint32_t x) {
+  if (CT == kCacheE4m3) return make_uint2(half_of_e4m3_lo(x), half_of_e4m3_hi(x));
+  const uint32_t u = x ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 c = __floats2half2_rn(1152.f, 1152.f);
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), c);
+  const __half2 e = __hsub2(*reinterpret_cast<const __half2*>(&b), c);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&d), *reinterpret_cast<const uint32_t*>(&e));
 }
 // Powers of two (f, 1 / f) with f top in [2^14, 2^15), f at most 2^103 (1 / f
 // times a softmax scale stays a normal number); (1, 1) where top is not finite.

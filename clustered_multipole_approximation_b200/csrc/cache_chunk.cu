@@ -164,11 +164,6 @@ __device__ inline void add2(uint64_t& s, const uint32_t* r) {
       : "+l"(s)
       : "r"(r[0]), "r"(r[1]));
 }
-__device__ inline float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
 // The wait for this thread's TMEM loads, tied to their registers so that no
 // use of them moves above it.
 __device__ inline void tld_wait(uint32_t* r) {
@@ -382,8 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         uint32_t y[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          y[2 * e] = K ? half_of_bytes<CT>(w[e], 0) : bf16_of_bytes<CT>(w[e], w[e], 0, 1);
-          y[2 * e + 1] = K ? half_of_bytes<CT>(w[e], 2) : bf16_of_bytes<CT>(w[e], w[e], 2, 3);
+          const uint2 z = K ? half_of_word<CT>(w[e]) : bf16_of_word<CT>(w[e]);
+          y[2 * e] = z.x;
+          y[2 * e + 1] = z.y;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e)

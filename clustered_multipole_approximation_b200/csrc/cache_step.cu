@@ -72,11 +72,14 @@ __device__ inline int q_column(int d) {
   return (d & 64) + 16 * k + 2 * t + (e & 1) + 8 * (e >> 1);
 }
 
-template <int CT, int D, int MT, bool CL>
+// MT m16 tiles of rows; with HR = 1 row half of the one tile (up to 8 rows): the
+// lanes' second rows are left out.
+template <int CT, int D, int MT, int HR, bool CL>
 __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_constant__ CacheAttn a) {
   using L = StepL<CT, D, MT>;
   constexpr int KB = L::KB, NT = KB / 8, DT = D / 8;
   constexpr bool k8 = L::SZ == 1;
+  constexpr int XE = 2 * HR;  // a lane's logits of an n8 tile that are used
   extern __shared__ __align__(128) unsigned char step_sm[];
   __shared__ float qback[L::ROWS];  // 8-bit: the power of two that undoes a row's factor
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -167,23 +170,23 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
     }
   }
   __syncthreads();
-  int2 see[MT][2];   // of rows 16 i + g and 16 i + g + 8
-  float mul[MT][2];  // their product to base-2 logit
+  int2 see[MT][HR];   // of rows 16 i + g and 16 i + g + 8
+  float mul[MT][HR];  // their product to base-2 logit
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < HR; ++e) {
       const int r = 16 * i + 8 * e + g;
       see[i][e] = seen(a, s, s.pos0 + r / a.G);
       see[i][e].y = min(see[i][e].y, t1);
       mul[i][e] = a.scale * kLog2e * (k8 ? qback[r] : 1.f);
     }
 
-  float o[MT][DT][4], m[MT][2], l[MT][2];  // l: this lane's share
+  float o[MT][DT][4], m[MT][HR], l[MT][HR];  // l: this lane's share
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    m[i][0] = m[i][1] = kFloor;
-    l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+    for (int e = 0; e < HR; ++e) m[i][e] = kFloor, l[i][e] = 0.f;
 #pragma unroll
     for (int j = 0; j < DT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
   }
@@ -228,9 +231,9 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t b0 = half_of_bytes<CT>(ww[e], 0), b1 = half_of_bytes<CT>(ww[e], 2);
+            const uint2 kk = half_of_word<CT>(ww[e]);
 #pragma unroll
-            for (int u = 0; u < MT; ++u) mma_f16(x[u][n], q[u][e % KS], b0, b1);
+            for (int u = 0; u < MT; ++u) mma_f16(x[u][n], q[u][e % KS], kk.x, kk.y);
           }
         }
       }
@@ -243,9 +246,8 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
 #pragma unroll
       for (int u = 0; u < MT; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (k8) x[u][n][e] *= e & 1 ? f.y : f.x;
-          x[u][n][e] *= mul[u][e >> 1];
+        for (int e = 0; e < XE; ++e) {
+          x[u][n][e] *= k8 ? mul[u][e >> 1] * (e & 1 ? f.y : f.x) : mul[u][e >> 1];
         }
     }
     const bool edge = tb < rt.alo || tb + KB > rt.ahi || tb + KB > t1;
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < XE; ++e)
             if (masked(u, n, e)) x[u][n][e] = -INFINITY;
       if (CT != kCacheI8 && (tb < rt.alo || tb + KB > rt.ahi)) {
         bool f = false;
@@ -270,15 +272,15 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
         bad = bad || __any_sync(0xffffffffu, f);
       }
     }
-    float top[MT][2];
+    float top[MT][HR];
     bool moves = false;
 #pragma unroll
     for (int u = 0; u < MT; ++u)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < HR; ++e) {
         float y = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) y = fmaxf(y, fmaxf(x[u][n][2 * e], x[u][n][2 * e + 1]));
+        for (int n = 0; n < NT; ++n) y = max3(y, x[u][n][2 * e], x[u][n][2 * e + 1]);
         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
         top[u][e] = y;
@@ -287,16 +289,19 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
     if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
-        float f[2];
+        float f[2] = {1.f, 1.f};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < HR; ++e) {
           const bool v = top[u][e] > m[u][e] + kSlack;
           f[e] = v ? fast_exp2(m[u][e] - top[u][e]) : 1.f;
           m[u][e] = v ? top[u][e] : m[u][e];
           l[u][e] *= f[e];
         }
 #pragma unroll
-        for (int j = 0; j < DT; ++j) o[u][j][0] *= f[0], o[u][j][1] *= f[0], o[u][j][2] *= f[1], o[u][j][3] *= f[1];
+        for (int j = 0; j < DT; ++j) {
+          o[u][j][0] *= f[0], o[u][j][1] *= f[0];
+          if (HR == 2) o[u][j][2] *= f[1], o[u][j][3] *= f[1];
+        }
       }
     }
 #pragma unroll
@@ -306,7 +311,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
 #pragma unroll
       for (int u = 0; u < MT; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < XE; ++e) {
           const float y = fast_exp2(x[u][n][e] - m[u][e >> 1]);
           l[u][e >> 1] += y;
           x[u][n][e] = k8 ? y * (e & 1 ? f.y : f.x) : y;
@@ -320,9 +325,9 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
         p[u][0] = bf16_bits2(x[u][2 * k][0], x[u][2 * k][1]);
-        p[u][1] = bf16_bits2(x[u][2 * k][2], x[u][2 * k][3]);
+        p[u][1] = HR == 2 ? bf16_bits2(x[u][2 * k][2], x[u][2 * k][3]) : 0;
         p[u][2] = bf16_bits2(x[u][2 * k + 1][0], x[u][2 * k + 1][1]);
-        p[u][3] = bf16_bits2(x[u][2 * k + 1][2], x[u][2 * k + 1][3]);
+        p[u][3] = HR == 2 ? bf16_bits2(x[u][2 * k + 1][2], x[u][2 * k + 1][3]) : 0;
       }
       if (!k8) {
 #pragma unroll
@@ -351,11 +356,14 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
           }
         }
 #pragma unroll
-        for (int j = 0; j < DT; ++j) {
-          const uint32_t b0 = bf16_of_bytes<CT>(v[0][j >> 2], v[1][j >> 2], j & 3, j & 3);
-          const uint32_t b1 = bf16_of_bytes<CT>(v[2][j >> 2], v[3][j >> 2], j & 3, j & 3);
+        for (int w = 0; w < W; ++w) {
+          uint32_t b0[4], b1[4];
+          bf16_pairs<CT>(v[0][w], v[1][w], b0);
+          bf16_pairs<CT>(v[2][w], v[3][w], b1);
 #pragma unroll
-          for (int u = 0; u < MT; ++u) mma_bf16(o[u][j], p[u], b0, b1);
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int u = 0; u < MT; ++u) mma_bf16(o[u][4 * w + j], p[u], b0[j], b1[j]);
         }
       }
     }
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
 #pragma unroll
     for (int u = 0; u < MT; ++u)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < HR; ++e) {
         l[u][e] += __shfl_xor_sync(0xffffffffu, l[u][e], 1);
         l[u][e] += __shfl_xor_sync(0xffffffffu, l[u][e], 2);
         const int r = 16 * u + 8 * e + g;
@@ -442,25 +450,35 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
   for (int e = split * 32 * kWarps + tid; e < rt.r1 * (D / 8); e += a.S * 32 * kWarps) {
     const int r = e / (D / 8), c = e % (D / 8);
     float mr = kFloor, lr = 0.f, y[8] = {};
-    for (int p = 0; p < parts; ++p) mr = fmaxf(mr, cluster.map_shared_rank(cml, p)[r].x);
-    for (int p = 0; p < parts; ++p) {
-      const float2 ml = cluster.map_shared_rank(cml, p)[r];
-      const float f = fast_exp2(ml.x - mr);
-      lr += ml.y * f;
-      float z[8];
-      load8_in(cluster.map_shared_rank(co, p) + r * D + 8 * c, z);
+    float2 ml[8];
+    float z[8][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = fmaf(z[i], f, y[i]);
+    for (int p = 0; p < 8; ++p) {  // every load on its way before the first is used
+      ml[p] = make_float2(kFloor, 0.f);
+      if (p < parts) {
+        ml[p] = cluster.map_shared_rank(cml, p)[r];
+        load8_in(cluster.map_shared_rank(co, p) + r * D + 8 * c, z[p]);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < 8; ++p) mr = fmaxf(mr, ml[p].x);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      if (p >= parts) break;
+      const float f = fast_exp2(ml[p].x - mr);
+      lr += ml[p].y * f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(z[p][i], f, y[i]);
     }
     finish(r, c, y, mr, lr);
   }
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-template <int CT, int D, int MT, bool CL>
+template <int CT, int D, int MT, int HR, bool CL>
 void launch(const CacheAttn& a, cudaStream_t st) {
   const int smem = StepL<CT, D, MT>::TOTAL;
-  auto* kernel = cache_step_kernel<CT, D, MT, CL>;
+  auto* kernel = cache_step_kernel<CT, D, MT, HR, CL>;
   static LargeShared allowed;
   allowed.ensure((const void*)kernel, smem);
   cudaLaunchConfig_t cfg{};
@@ -478,10 +496,12 @@ void launch(const CacheAttn& a, cudaStream_t st) {
 }
 template <int CT, int D>
 void launch_as(const CacheAttn& a, cudaStream_t st) {
-  if (a.rows == 16)
-    a.cluster ? launch<CT, D, 1, true>(a, st) : launch<CT, D, 1, false>(a, st);
+  if (a.rows == 8)
+    a.cluster ? launch<CT, D, 1, 1, true>(a, st) : launch<CT, D, 1, 1, false>(a, st);
+  else if (a.rows == 16)
+    a.cluster ? launch<CT, D, 1, 2, true>(a, st) : launch<CT, D, 1, 2, false>(a, st);
   else
-    a.cluster ? launch<CT, D, 2, true>(a, st) : launch<CT, D, 2, false>(a, st);
+    a.cluster ? launch<CT, D, 2, 2, true>(a, st) : launch<CT, D, 2, 2, false>(a, st);
 }
 
 }  // namespace

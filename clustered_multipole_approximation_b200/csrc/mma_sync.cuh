@@ -65,6 +65,13 @@ __device__ inline float fast_exp2(float x) {
   return y;
 }
 
+// Largest of three (the numbers among them).
+__device__ inline float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 // Running maxima start at a finite floor so that fully masked blocks need no
 // special case: exp2(-inf - floor) = 0 and exp2(floor - floor) = 1.
 constexpr float kMaxFloor = -1.0e30f;
