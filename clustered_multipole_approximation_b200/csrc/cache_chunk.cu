@@ -16,14 +16,23 @@
 //
 // Pages are gathered by four load warps: a lane looks up the page row of one
 // key, the warp copies whole rows into the 128-byte-swizzled operand form
-// (cp.async; 8-bit rows are converted to bf16, exact, on the way).  Any page
-// size is the same to them.  Scales of 8-bit rows multiply S's and P's
-// columns.
+// (cp.async), so that any page size is the same to them.  8-bit rows come
+// through a raw ring and are converted on the way, exactly: V to bf16, K to fp16
+// (half the instructions), which Q's rows, brought into fp16's range by powers
+// of two, then are as well.  Scales of 8-bit rows multiply S's and P's columns.
 //
 // Warps 0-7: softmax of stream 0 (0-3) and 1 (4-7); 8-11: loads; 12: products.
 // One warp issues all products, the streams in turn: that keeps them half a
 // step apart (two issuing warps drift into step, softmax against softmax).
 // Every wait is bounded; one that gives up sets kErrMmaWait.
+//
+// What bounds it: a stream's chain S -> maximum -> exponentials -> P V -> S,
+// about 3300 cycles a tile pair at D = 128 where the products alone take 2100.
+// 2048 tokens of 32 heads (8 kv-heads of 128) at 32768: 940 us in a short run,
+// 1.13 PFLOP/s.  Tried and slower: tiles of 64 keys with two S buffers (the
+// smaller products run at half rate: 1221 us against 1122), four softmax
+// warpgroups (1223 against 1124), a polynomial for part of the exponentials
+// (1145 against 977: instructions, not the special-function unit, are short).
 #include "cache_attn.cuh"
 #include "kernels.h"
 #include "mma_sync.cuh"
@@ -146,18 +155,22 @@ __device__ inline void tst16(uint32_t taddr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Two fp32 at a time: r[0..1] *= (a, b); r[0..1] = r a + b; s += r.
+// Two fp32 at a time: r[0..1] *= (a, b); r[0..1] = r aa + bb; s += r.
 __device__ inline void mul2(uint32_t* r, float a, float b) {
   asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
       "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
       : "+r"(r[0]), "+r"(r[1])
       : "f"(a), "f"(b));
 }
-__device__ inline void fma2(uint32_t* r, float a, float b) {
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
-      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+__device__ inline void fma2(uint32_t* r, uint64_t aa, uint64_t bb) {
+  asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%0, %1};\n\tfma.rn.f32x2 x, x, %2, %3;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
       : "+r"(r[0]), "+r"(r[1])
-      : "f"(a), "f"(b));
+      : "l"(aa), "l"(bb));
+}
+__device__ inline uint64_t twice(float a) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %1};\n" : "=l"(x) : "f"(a));
+  return x;
 }
 __device__ inline void add2(uint64_t& s, const uint32_t* r) {
   asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tadd.rn.f32x2 %0, %0, x;\n\t}\n"
@@ -325,11 +338,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       constexpr int LPR = D / 8, RPI = 32 / LPR;
       const int q = lane % LPR;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(base) + 8 * q;
-#pragma unroll 8
-      for (int j = 0; j < 32 / RPI; ++j) {
-        const int r = j * RPI + lane / LPR;
-        const int pr = __shfl_sync(0xffffffffu, row, r);
-        cp16(st + (q >> 3) * L::QC + swz(32 * lw + r, q & 7), src + (long long)max(pr, 0) * D, pr < 0 ? 0 : 16);
+      if (__all_sync(0xffffffffu, row >= 0)) {
+#pragma unroll
+        for (int j = 0; j < 32 / RPI; ++j) {
+          const int r = j * RPI + lane / LPR;
+          cp16(st + (q >> 3) * L::QC + swz(32 * lw + r, q & 7), src + (long long)__shfl_sync(0xffffffffu, row, r) * D);
+        }
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < 32 / RPI; ++j) {
+          const int r = j * RPI + lane / LPR;
+          const int pr = __shfl_sync(0xffffffffu, row, r);
+          cp16(st + (q >> 3) * L::QC + swz(32 * lw + r, q & 7), src + (long long)max(pr, 0) * D, pr < 0 ? 0 : 16);
+        }
       }
       cp_commit();
     };
@@ -351,10 +372,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         const int row = k || fetched == 2 * nt - 1 ? row_cur : row_prev;
         unsigned char* dst = raw + (fetched % L::RS) * L::RAWW;
         const unsigned char* src = static_cast<const unsigned char*>(k ? a.c.k : a.c.v) + 16 * (lane % LPR8);
+        if (__all_sync(0xffffffffu, row >= 0)) {
 #pragma unroll
-        for (int j = 0; j < N8; ++j) {
-          const int pr = __shfl_sync(0xffffffffu, row, j * RPI8 + lane / LPR8);
-          cp16(dst + (j * 32 + lane) * 16, src + (long long)max(pr, 0) * D, pr < 0 ? 0 : 16);
+          for (int j = 0; j < N8; ++j)
+            cp16(dst + (j * 32 + lane) * 16,
+                 src + (long long)__shfl_sync(0xffffffffu, row, j * RPI8 + lane / LPR8) * D);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < N8; ++j) {
+            const int pr = __shfl_sync(0xffffffffu, row, j * RPI8 + lane / LPR8);
+            cp16(dst + (j * 32 + lane) * 16, src + (long long)max(pr, 0) * D, pr < 0 ? 0 : 16);
+          }
         }
         if (k) {
           cp4(dst + 32 * D + 8 * lane, a.c.ks + max(row, 0), row < 0 ? 0 : 4);
@@ -514,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     const float sl2 = a.scale * kLog2e * (k8 ? qback[two ? 128 * w + row : row] : 1.f);
     const bool pos = a.scale > 0.f;
     const float mul = pos ? sl2 : 1.f;
+    const uint64_t mul2x = twice(mul);
     float m = kFloor, l = 0.f;
     const int n = steps(w);
     const bool idle = !__any_sync(0xffffffffu, live);
@@ -555,10 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       uint32_t p[32];
       // weights of columns [c0, c0 + 64) from their logits
       auto weights = [&](int c0) {
+        const uint64_t mm = twice(-m);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int c = c0 + 2 * e;
-          fma2(x + c, mul, -m);
+          fma2(x + c, mul2x, mm);
           x[c] = __float_as_uint(fast_exp2(__uint_as_float(x[c])));
           x[c + 1] = __float_as_uint(fast_exp2(__uint_as_float(x[c + 1])));
           add2(sum[e & 1], x + c);
@@ -604,42 +634,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         }
         if (f) sbad = 1;
       }
+      logits(0);
       logits(64);
-      float top2 = -INFINITY;
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 64; c < kKeys; c += 2) top2 = max3(top2, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-      for (;;) {
-        // The first half's weights with the maximum so far, next to the tile's own:
-        // the special-function unit need not wait for it.  Where the maximum has to
-        // move they are formed again, from S as it still lies in TMEM.
-        logits(0);
-        float mx[2] = {top2, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 64; c += 2)
-          mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-        sum[0] = sum[1] = 0;
-        weights(0);
-        const float top = fmaxf(mx[0], mx[1]) * mul;
-        const bool move = top > m + kSlack;
-        if (!__any_sync(0xffffffffu, move)) break;
+      for (int c = 0; c < kKeys; c += 2)
+        mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+      const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * mul;
+      const bool move = top > m + kSlack;
+      if (__any_sync(0xffffffffu, move)) {
         const float f = move ? fast_exp2(m - top) : 1.f;
         m = move ? top : m;
         l *= f;
         if (k > 0) {  // the stream's last P V is done: S came after it
 #pragma unroll 1
           for (int d = 0; d < D; d += 32) {
-            tld32(tO + d, x);
-            tld_wait(x);
+            uint32_t r[32];
+            tld32(tO + d, r);
+            tld_wait(r);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) mul2(x + e, f, f);
-            tst32(tO + d, x);
+            for (int e = 0; e < 32; e += 2) mul2(r + e, f, f);
+            tst32(tO + d, r);
           }
         }
-        tld32(tS, x);
-        tld32(tS + 32, x + 32);
-        tld_wait(x);
-        tld_wait(x + 32);
       }
+      sum[0] = sum[1] = 0;
+      weights(0);
       store(0);
       weights(64);
       store(1);
