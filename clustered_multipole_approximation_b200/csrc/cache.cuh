@@ -176,6 +176,7 @@ struct CacheAttn {
   int rows;       // packed rows of a tile
   int S;          // splits a row tile can have
   int minc;       // keys of a split, at least
+  int quantum;    // a split's keys are a multiple of this
   int PR;         // rows of a split's partial
   int cluster;    // the splits of a tile are a cluster and join by themselves
   void* ws;       // partial o, then ml

@@ -8,66 +8,77 @@
 // running maximum m and sum l, and o rescaled when m moves.
 #include "cache_attn.cuh"
 #include "kernels.h"
+#include "mma_sync.cuh"
 
 namespace muse {
 
 namespace {
 
-// Joins the splits of one row: W warps take every W-th split each, then the
-// CTA's first warp their sums, always in this order.
+// Joins the splits of a row: W warps take every W-th split each, then the first
+// of them their sums, always in this order.  A CTA has eight warps.
 template <typename T, int D, int W>
-__global__ void __launch_bounds__(32 * W) cache_join_kernel(const __grid_constant__ CacheAttn a) {
+__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ CacheAttn a, int total) {
   constexpr int C = D / 32;  // columns of a lane
-  __shared__ float so[W][D];
-  __shared__ float2 sml[W];
-  const int n = a.c.n, rows = n * a.G;
-  const long long bh = blockIdx.x / rows;
-  const int r = (int)(blockIdx.x - bh * rows);
-  const int b = (int)(bh / a.c.Hkv), h = (int)(bh - (long long)b * a.c.Hkv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const SeqLen s = seq_len(a.c, b);
+  __shared__ float so[8][D];
+  __shared__ float2 sml[8];
+  const int rows = a.c.n * a.G;  // of a kv-head
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
+  const long long gr = (long long)blockIdx.x * (8 / W) + warp / W;
+  const int bh = (int)(gr / rows), r = (int)(gr - (long long)bh * rows);
+  const int b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
+  const bool there = gr < total;
+  SeqLen s{};
+  if (there) s = seq_len(a.c, b);
   cudaGridDependencySynchronize();
-  if (r >= s.nn * a.G) return;
+  bool live = there && r < s.nn * a.G;
   const int rt = r / a.rows;
-  const RowTile t = row_tile(a, s, rt * a.rows, a.rows);
-  const int parts = split_count(a, t.hi - t.lo);
-  if (parts == 1) return;  // the tile wrote its rows itself
-  const long long tile = bh * a.RT + rt;
+  RowTile t{};
+  int parts = 1;
+  if (live) {
+    t = row_tile(a, s, rt * a.rows, a.rows);
+    parts = split_count(a, t.hi - t.lo);
+    live = parts > 1;  // else the tile wrote its rows itself
+  }
+  const long long tile = (long long)bh * a.RT + rt;
   const int pr = r - t.r0;
   float m = kFloor, l = 0.f, o[C] = {};
+  if (live) {
 #pragma unroll 4
-  for (int p = warp; p < parts; p += W) {
-    const float2 ml = *part_ml(a, tile, p, pr);
-    const float* po = part_o<D>(a, tile, p, pr) + C * lane;
-    float y[C];
+    for (int p = part; p < parts; p += W) {
+      const float2 ml = *part_ml(a, tile, p, pr);
+      const float* po = part_o<D>(a, tile, p, pr) + C * lane;
+      float y[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) y[c] = po[c];
-    // NaN maxima do not arise: they are maxima of the numbers among the logits
-    const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), g = exp2f(ml.x - mn);
-    l = l * f + ml.y * g;
+      for (int c = 0; c < C; ++c) y[c] = po[c];
+      // NaN maxima do not arise: they are maxima of the numbers among the logits
+      const float mn = fmaxf(m, ml.x), f = fast_exp2(m - mn), g = fast_exp2(ml.x - mn);
+      l = l * f + ml.y * g;
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = o[c] * f + y[c] * g;
-    m = mn;
+      for (int c = 0; c < C; ++c) o[c] = o[c] * f + y[c] * g;
+      m = mn;
+    }
   }
   if (W > 1) {
 #pragma unroll
     for (int c = 0; c < C; ++c) so[warp][C * lane + c] = o[c];
     if (lane == 0) sml[warp] = make_float2(m, l);
     __syncthreads();
-    if (warp) return;
+    if (part) return;
     m = kFloor;
     l = 0.f;
-    for (int w = 0; w < W; ++w) m = fmaxf(m, sml[w].x);
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = fmaxf(m, sml[warp + w].x);
 #pragma unroll
     for (int c = 0; c < C; ++c) o[c] = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float f = exp2f(sml[w].x - m);
-      l += sml[w].y * f;
+      const float f = fast_exp2(sml[warp + w].x - m);
+      l += sml[warp + w].y * f;
 #pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = fmaf(so[w][C * lane + c], f, o[c]);
+      for (int c = 0; c < C; ++c) o[c] = fmaf(so[warp + w][C * lane + c], f, o[c]);
     }
   }
+  if (!live) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const RowAt at = row_at(a, b, h, r);
   T* op = static_cast<T*>(a.O) + at.o + C * lane;
@@ -79,24 +90,26 @@ __global__ void __launch_bounds__(32 * W) cache_join_kernel(const __grid_constan
 template <typename T, int D, int W>
 void join_as(const CacheAttn& a, cudaStream_t st) {
   // launched while its predecessor drains: it waits for it on the device
+  const int rows = a.B * a.Hq * a.c.n;  // < 2^31, checked
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hq * a.c.n));
-  cfg.blockDim = dim3(32 * W);
+  cfg.gridDim = dim3((unsigned)(((long long)rows * W + 7) / 8));
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D, W>, a);
+  cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D, W>, a, rows);
+}
+template <typename T, int D>
+void join_of(const CacheAttn& a, cudaStream_t st) {
+  a.S <= 8 ? join_as<T, D, 1>(a, st) : a.S <= 32 ? join_as<T, D, 4>(a, st) : join_as<T, D, 8>(a, st);
 }
 template <typename T>
 void run_join(const CacheAttn& a, cudaStream_t st) {
   ProfScope ps(st, "cache_join");
-  if (a.c.D == 64)
-    a.S <= 8 ? join_as<T, 64, 1>(a, st) : join_as<T, 64, 8>(a, st);
-  else
-    a.S <= 8 ? join_as<T, 128, 1>(a, st) : join_as<T, 128, 8>(a, st);
+  a.c.D == 64 ? join_of<T, 64>(a, st) : join_of<T, 128>(a, st);
 }
 
 enum Path { kWide, kStep, kChunk };
@@ -121,10 +134,25 @@ Path plan(CacheAttn& a) {
   const long long units = (long long)a.B * a.c.Hkv * a.RT;
   a.S = a.minc = 1;
   a.cluster = 0;
-  if (p != kChunk) {
+  a.quantum = p == kWide ? 64 : kQuantum;
+  if (p == kWide) {
+    // in blocks of 64 keys: two CTAs an SM at a time, half a wave lost at the end,
+    // 0.3 of a block for a split's start and partials
+    double best = 1e30;
+    for (int S = 1; S <= 64 && (S == 1 || (long long)S * 64 < cap + 64); ++S) {
+      if (S > 1 && units * S > 0x7FFFFFFF) break;
+      const double waves = (double)(units * S) / (2 * kSMs);
+      const double w = ((waves < 0.5 ? 0.5 : waves) + 0.5) * ((double)((cap + S * 64LL - 1) / (S * 64LL)) + 0.3);
+      if (w < best - 1e-9) {
+        best = w;
+        a.S = S;
+      }
+    }
+    a.minc = 64;
+  } else if (p == kStep) {
     // keys of a split: enough splits for eight CTAs an SM, none of more than
     // 512 KB of cache, and no more than 128 a row
-    const int size = a.type == kCacheF32 ? 4 : a.type == kCacheBf16 ? 2 : 1;
+    const int size = a.type == kCacheBf16 ? 2 : 1;
     long long c = quanta(cap * units / (kSMs * 8) + 1);
     const long long most = quanta((512 << 10) / (2 * a.c.D * size));
     if (c > most) c = most;
@@ -134,7 +162,7 @@ Path plan(CacheAttn& a) {
     // a table far wider than its sequences: shorter splits while few rows fill the SMs
     const long long least = quanta(c * units / (2 * kSMs));
     a.minc = (int)(least < c ? least : c);
-    if (p == kStep && a.S > 1 && a.S <= 16) {  // up to eight join without a second launch
+    if (a.S > 1 && a.S <= 16) {  // up to eight join without a second launch
       a.S = a.S < 8 ? a.S : 8;
       a.cluster = 1;
     }

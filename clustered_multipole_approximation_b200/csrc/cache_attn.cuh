@@ -21,7 +21,7 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 // exp2(-inf - floor) = 0.
 constexpr float kFloor = -3.0e38f;
 constexpr float kSlack = 8.f;  // the maximum moves when a logit exceeds it by this (base 2)
-constexpr int kQuantum = 128;  // splits begin at multiples of this from the range's start
+constexpr int kQuantum = 128;  // keys: splits are multiples of it (64 on the fp32 path)
 
 // A row tile: packed rows [r0, r1) of (b, h) and the keys that any (all) of
 // them see.
@@ -46,7 +46,7 @@ __host__ __device__ inline int round_up(int x, int m) { return (x + m - 1) / m *
 // Keys of one split of a range of len keys: the call has up to a.S splits for
 // every row tile, a tile uses as many as its own length asks for.
 __device__ inline int split_keys(const CacheAttn& a, int len) {
-  return max(a.minc, round_up((len + a.S - 1) / a.S, kQuantum));
+  return max(a.minc, round_up((len + a.S - 1) / a.S, a.quantum));
 }
 __device__ inline int split_count(const CacheAttn& a, int len) {
   const int c = split_keys(a, len);

@@ -126,12 +126,12 @@ __global__ void __launch_bounds__(256) cache_wide_kernel(const __grid_constant__
       }
 #pragma unroll
       for (int w = 1; w < 16; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-      const float mn = fmaxf(m[i], top), f = exp2f(m[i] - mn);
+      const float mn = fmaxf(m[i], top), f = fast_exp2(m[i] - mn);
       m[i] = mn;
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float e = exp2f(acc[i][j] - mn);
+        const float e = fast_exp2(acc[i][j] - mn);
         sum += e;
         wide_sm[L::P + (y * RT + i) * L::PS + x + 16 * j] = e;
       }
