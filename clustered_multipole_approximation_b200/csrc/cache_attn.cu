@@ -157,6 +157,8 @@ Path plan(CacheAttn& a) {
     const long long most = quanta((512 << 10) / (2 * a.c.D * size));
     if (c > most) c = most;
     if (c * 128 < cap) c = quanta((cap + 127) / 128);
+    // (and no more than 64 CTAs an SM in all: workspace for nothing)
+    if (c * (kSMs * 64) < cap * units) c = quanta(cap * units / (kSMs * 64));
     a.S = (int)((cap + c - 1) / c);
     while (a.S > 1 && units * a.S > 0x7FFFFFFF) a.S = (a.S + 1) / 2;  // the grid
     // a table far wider than its sequences: shorter splits while few rows fill the SMs

@@ -674,8 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
 
     // ---- the rows: joined streams, normalised (or a split's partial) --------------
     float* jo = reinterpret_cast<float*>(sm + L::STAGES);  // [column][row]; every load was used
+    streams_sync();  // both streams' products are done
     if (!two) {
-      streams_sync();  // both streams' products are done
       if (w == 1 && n > 0) {
 #pragma unroll
         for (int d = 0; d < D; d += 32) {
@@ -701,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         l = l * f0 + ml.y * f1;
       }
       const RowAt at = row_at(a, b, h, live ? pr : r0);
+      if (sfail) l = m = __int_as_float(0x7FC00000);  // a wait gave up: no numbers, whoever reads the flag
       const float inv = parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.O) + at.o;
 #pragma unroll

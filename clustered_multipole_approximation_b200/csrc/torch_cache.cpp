@@ -63,7 +63,7 @@ void on(const at::Tensor* t, const char* name, c10::Device dev) {
 // device's current one.
 struct Place {
   c10::cuda::CUDAStream stream;
-  bool other = false;  // not the current stream: what is allocated here is marked as used on it
+  bool other = false;  // not the current stream: the call's tensors are marked as used on it
   std::optional<c10::cuda::CUDAGuard> guard;
 
   Place(c10::Device dev, PyObject* s) : stream(c10::cuda::getCurrentCUDAStream(dev.index())) {
@@ -78,8 +78,15 @@ struct Place {
     }
     if (c10::cuda::current_device() != dev.index()) guard.emplace(dev);
   }
-  void uses(const at::Tensor& made) const {
-    if (other) made.record_stream(stream.unwrap());
+  void uses(const at::Tensor& t) const {
+    if (other) t.record_stream(stream.unwrap());
+  }
+  // every tensor among a call's arguments: its owner may let go of it before
+  // the other stream has read it
+  void uses_arguments(PyObject* const* o, Py_ssize_t n) const {
+    if (!other) return;
+    for (Py_ssize_t i = 0; i < n; ++i)
+      if (THPVariable_Check(o[i])) uses(THPVariable_Unpack(o[i]));
   }
 };
 
@@ -220,6 +227,7 @@ PyObject* cache_write(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const muse_strides ks = strides(k, "k"), vs = strides(v, "v");
     int32_t* err = error_word(maybe(o[9], "device_error"), a.dev);
     const Place p(a.dev, o[10]);
+    p.uses_arguments(o, n);
     check(muse_cache_write(k.data_ptr(), &ks, v.data_ptr(), &vs, &sh, &a.ca, &a.ix, err, p.stream.stream()));
     Py_RETURN_NONE;
   });
@@ -239,6 +247,7 @@ PyObject* cache_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
     on(start, "start", a.dev);
     const int32_t* sp = index_array(start, "start", B);
     const Place p(a.dev, o[12]);
+    p.uses_arguments(o, n);
     at::Tensor k, v;
     if (o[9] == Py_None) {
       const auto opt = at::TensorOptions().device(a.dev).dtype(o[8] == Py_True ? at::kBFloat16 : at::kFloat);
@@ -305,6 +314,7 @@ PyObject* attn_cache(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const muse_strides qs = strides(q, "q");
     int32_t* err = error_word(maybe(o[14], "device_error"), a.dev);
     const Place p(a.dev, o[15]);
+    p.uses_arguments(o, n);
 
     at::Tensor out, lse, ws;
     if (o[11] == Py_None) {

@@ -452,7 +452,8 @@ muse_status muse_cache_read(void *K, void *V, const muse_shape *shape, const mus
  * fp32 contiguous or NULL; O and lse share no memory with Q.  Logits and sums
  * are fp32; for bf16 queries the softmax weights are rounded once to bf16 for
  * the tensor cores (an 8-bit cache's row scale multiplied in first).  The same
- * call on the same inputs gives the same bits.
+ * call on the same inputs gives the same bits.  Calls that may run at the same
+ * time (other streams, captured graphs) need workspaces of their own.
  */
 size_t muse_attn_cache_workspace_size(const muse_shape *shape, const muse_cache *cache,
                                       const muse_cache_index *index);
