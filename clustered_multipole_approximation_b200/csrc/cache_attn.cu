@@ -120,12 +120,11 @@ Path path_of(const CacheAttn& a) {
 
 constexpr int kSMs = 148;
 
-// How the call's keys are divided, from its sizes alone (the lengths are on
-// the device; each row tile then uses the splits that its own length asks
-// for).
-Path plan(CacheAttn& a) {
+// How up to `cap` keys of a row tile are divided, from the call's sizes alone
+// (the lengths are on the device; each row tile then uses the splits that its
+// own length asks for).
+Path plan_keys(CacheAttn& a, long long cap) {
   const Path p = path_of(a);
-  const long long cap = (long long)a.c.wide * a.c.page.d;
   const long long packed = (long long)a.c.n * a.G;
   auto quanta = [](long long x) { return (x + kQuantum - 1) / kQuantum * kQuantum; };
   a.rows = p == kChunk ? 256 : p == kStep && packed <= 8 ? 8 : packed <= 16 ? 16 : p == kStep ? 32 : 64;
@@ -181,6 +180,25 @@ Path plan(CacheAttn& a) {
       if (units * S > 8 * kSMs) break;
     }
     a.minc = 512;
+  }
+  return p;
+}
+
+// The division for the call's keys: what its table can hold, or what a tile's
+// rows can see through the window.  The workspace is sized without the window,
+// so that a windowed call takes no more of it.
+Path plan(CacheAttn& a) {
+  const long long cap = (long long)a.c.wide * a.c.page.d;
+  const Path p = plan_keys(a, cap);
+  const long long reach = (long long)a.window + a.rows / a.G + 1;
+  if (!a.window || reach >= cap) return p;
+  const int S = a.S, cluster = a.cluster;
+  plan_keys(a, reach);
+  if (S == 1 || (cluster && !a.cluster)) {
+    a.S = 1;
+    a.cluster = 0;
+  } else if (!a.cluster && a.S > S) {
+    a.S = S;
   }
   return p;
 }

@@ -267,6 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       asm volatile("fence.mbarrier_init.release.cluster;\n");
     }
   }
+  const int lw = warp - 8;  // of a load warp: its keys of a tile are 32 lw + lane
+  auto lookup = [&](int T) -> int {
+    const int t = t0 + T * kKeys + 32 * lw + lane;
+    return T < nt && t < t1 ? (int)row_of(a.c, b, h, t) : -1;
+  };
+  const int first = warp >= 8 && warp < 12 ? lookup(0) : -1;  // on its way beside the queries
   {  // the query rows; rows past the tile are zero
     const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
     constexpr int P = D / 8;  // 16-byte pieces of a row
@@ -309,11 +315,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
   if (warp >= 8 && warp < 12) {
     // ---- loads -----------------------------------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
-    const int lw = warp - 8;  // this warp's keys of a tile: 32 lw + lane
-    auto lookup = [&](int T) -> int {
-      const int t = t0 + T * kKeys + 32 * lw + lane;
-      return T < nt && t < t1 ? (int)row_of(a.c, b, h, t) : -1;
-    };
     auto report = [&](int item) {
       fence_async();
       __syncwarp();
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     // thread's own (it converts the bytes that it copied)
     constexpr int LPR8 = D / 16, RPI8 = 32 / LPR8, N8 = 32 / RPI8;
     unsigned char* raw = sm + L::RAW + lw * (L::RS * L::RAWW);
-    int fetched = 0, row_next = k8 ? lookup(0) : -1, row_cur = -1, row_prev = -1;
+    int fetched = 0, row_next = first, row_cur = -1, row_prev = -1;
     auto is_k = [&](int item) { return item == 0 || ((item & 1) && item < 2 * nt - 1); };
     auto fetch = [&]() {
       if (fetched < 2 * nt) {
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           report(item);
         }
       } else {
-        int rk = lookup(0), rv = rk;  // page rows of the next K and the next V
+        int rk = first, rv = rk;  // page rows of the next K and the next V
         auto pump = [&]() {
           ++issued;
           cp_wait<L::LAG>();
@@ -576,8 +577,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         }
         if (edge) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c0 + c < clo || c0 + c >= chi) y[c] = 0xFF800000u;
+          for (int q = 0; q < 64; q += 32) {
+            // most quarters are seen by all of the warp's rows, or up to one end
+            if (__all_sync(0xffffffffu, c0 + q >= clo && c0 + q + 32 <= chi)) continue;
+#pragma unroll
+            for (int c = q; c < q + 32; ++c)
+              if (c0 + c < clo || c0 + c >= chi) y[c] = 0xFF800000u;
+          }
         }
       };
       uint64_t sum[2];
@@ -626,13 +632,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       if (CT != kCacheI8 && (tb < alo || tb + kKeys > ahi)) {
         // values that are not numbers would reach the rows that do not see them
         wait(mFull[vi % NS], vi / NS);
-        bool f = false;
-        const unsigned char* sv = sm + L::STAGES + (vi % NS) * L::SS;
-        for (int e = row; e < L::SS / 16; e += 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sv + 16 * e);
-          f = f || bf16_not_finite(u.x) || bf16_not_finite(u.y) || bf16_not_finite(u.z) || bf16_not_finite(u.w);
+        constexpr int P = D / 8, RP = 128 / P;  // pieces of a key, keys of a pass
+        const int c = row % P;
+        const unsigned char* sv = sm + L::STAGES + (vi % NS) * L::SS + (c >> 3) * L::QC;
+        uint32_t f = 0;  // a half's upper bit: its exponent is all ones
+#pragma unroll 4
+        for (int r = row / P; r < kKeys; r += RP) {
+          if (tb + r >= alo && tb + r < ahi) continue;  // every row sees it
+          const uint4 u = *reinterpret_cast<const uint4*>(sv + swz(r, c & 7));
+          f |= ((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
+               ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u);
         }
-        if (f) sbad = 1;
+        if (f & 0x80008000u) sbad = 1;
       }
       logits(0);
       logits(64);
