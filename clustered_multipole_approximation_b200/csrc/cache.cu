@@ -3,9 +3,14 @@
 // Both are one pass over the bytes: D / 16 lanes hold a row, two pieces of eight
 // values each (D / 2 columns apart, so that neighbouring lanes touch
 // neighbouring bytes), so that a row's largest magnitude is a shuffle reduction
-// in registers and every load and store is 8 to 32 bytes a lane.  K and V of a row go through
-// the same thread (two independent chains of loads).  Bound by HBM where the
-// call is large, by the launch where it is one token a sequence.
+// in registers and every load and store is 8 to 32 bytes a lane.  K and V of a
+// row go through the same lanes (independent chains of loads).
+//
+// Bound by HBM where nothing is converted (32768 rows of 8 heads of 128, bf16:
+// 45 us each way, 5.9 TB/s, 90 % of a copy's rate), by instructions beside it
+// where rows are quantised (the same rows in int8: write 53 us, 3.9 TB/s; read
+// 41 us, 4.9 TB/s; e4m3 of 64: write 21 us, 5.0 TB/s), by the launch where it is
+// one token a sequence (4 us).  A piece a lane instead of two took 62 and 44 us.
 #include "cache.cuh"
 #include "kernels.h"
 
