@@ -208,6 +208,7 @@ struct ChunkL {
   static constexpr int RS = D == 128 ? 3 : 6;  // 8-bit: raw loads on their way, and the bytes of
   static constexpr int RAWW = 32 * D + 32 * 8;  // a load warp's share of one (rows, scales)
   static constexpr int RAW = SC + (CT == kCacheBf16 ? 0 : kScales * 2 * kKeys * 4);
+  static constexpr int JOIN = D * 128 * 4 + 128 * 8;  // the second stream's o, (m, l)
   static constexpr int TOTAL = RAW + (CT == kCacheBf16 ? 0 : 4 * RS * RAWW) + 1024;
 };
 
@@ -222,7 +223,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
   __shared__ __align__(8) uint64_t mFull[NS], mEmpty[NS], mS[2], mP[2][2], mO[2];
   __shared__ uint32_t tslot;
   __shared__ int sbad, sfail;
-  __shared__ float2 jml[128];
   __shared__ float qback[k8 ? 256 : 1];  // 8-bit: the power of two that undoes a row's factor
 
   const long long tile = blockIdx.x / a.S;
@@ -578,11 +578,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         if (edge) {
 #pragma unroll
           for (int q = 0; q < 64; q += 32) {
-            // most quarters are seen by all of the warp's rows, or up to one end
-            if (__all_sync(0xffffffffu, c0 + q >= clo && c0 + q + 32 <= chi)) continue;
+            // bit c: this row sees column c0 + q + c; most quarters are seen by every
+            // row of the warp, or by none
+            const int lo = min(max(clo - c0 - q, 0), 32), hi = min(max(chi - c0 - q, 0), 32);
+            const uint32_t seen_cols = lo < hi ? (0xFFFFFFFFu >> (32 - hi)) & (0xFFFFFFFFu << lo) : 0u;
+            if (__all_sync(0xffffffffu, seen_cols == 0xFFFFFFFFu)) continue;
 #pragma unroll
-            for (int c = q; c < q + 32; ++c)
-              if (c0 + c < clo || c0 + c >= chi) y[c] = 0xFF800000u;
+            for (int c = 0; c < 32; ++c)
+              if (!(seen_cols & (1u << c))) y[q + c] = 0xFF800000u;
           }
         }
       };
@@ -636,12 +639,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         const int c = row % P;
         const unsigned char* sv = sm + L::STAGES + (vi % NS) * L::SS + (c >> 3) * L::QC;
         uint32_t f = 0;  // a half's upper bit: its exponent is all ones
-#pragma unroll 4
+#pragma unroll 8
         for (int r = row / P; r < kKeys; r += RP) {
-          if (tb + r >= alo && tb + r < ahi) continue;  // every row sees it
           const uint4 u = *reinterpret_cast<const uint4*>(sv + swz(r, c & 7));
-          f |= ((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
-               ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u);
+          const uint32_t z = ((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
+                             ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u);
+          f |= tb + r >= alo && tb + r < ahi ? 0 : z;  // (a key that every row sees may be anything)
         }
         if (f & 0x80008000u) sbad = 1;
       }
@@ -685,6 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
 
     // ---- the rows: joined streams, normalised (or a split's partial) --------------
     float* jo = reinterpret_cast<float*>(sm + L::STAGES);  // [column][row]; every load was used
+    float2* jml = reinterpret_cast<float2*>(jo + D * 128);
+    // then the tile's rows, to be stored line by line
+    unsigned char* rows_sm = sm + L::STAGES + (two ? 0 : L::JOIN);
+    const int pitch = (parts > 1 ? 4 : 2) * D + 16;
     streams_sync();  // both streams' products are done
     if (!two) {
       if (w == 1 && n > 0) {
@@ -711,11 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         m = mn;
         l = l * f0 + ml.y * f1;
       }
-      const RowAt at = row_at(a, b, h, live ? pr : r0);
       if (sfail) l = m = __int_as_float(0x7FC00000);  // a wait gave up: no numbers, whoever reads the flag
       const float inv = parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.O) + at.o;
-#pragma unroll
+      unsigned char* to = rows_sm + (two ? 128 * w + row : row) * pitch;
+#pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t r[32];
         if (n > 0) {
@@ -725,7 +731,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = 0;
         }
-        if (!live) continue;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float y[8];
@@ -736,17 +741,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
             y[e] *= inv;
           }
           if (parts > 1)
-            store8(part_o<D>(a, tile, split, pr - r0) + d + 8 * c, y);
+            store8(reinterpret_cast<float*>(to) + d + 8 * c, y);
           else
-            store8(op + d + 8 * c, y);
+            store8(reinterpret_cast<__nv_bfloat16*>(to) + d + 8 * c, y);
         }
       }
       if (live) {
         if (parts > 1)
           *part_ml(a, tile, split, pr - r0) = make_float2(m, l);
         else if (a.lse)
-          a.lse[at.lse] = lse_of(m, l);
+          a.lse[row_at(a, b, h, pr).lse] = lse_of(m, l);
       }
+    }
+    streams_sync();
+    // whole rows from there: a lane's own row to global memory would touch 32 lines
+    // a store (up to 8000 cycles a tile, 16 % of it)
+    const int pieces = (parts > 1 ? 4 : 2) * D / 16;
+    for (int e = tid; e < (rt.r1 - r0) * pieces; e += 256) {
+      const int r = e / pieces, c = e - r * pieces;
+      const uint4 v = *reinterpret_cast<const uint4*>(rows_sm + r * pitch + 16 * c);
+      if (parts > 1)
+        *reinterpret_cast<uint4*>(part_o<D>(a, tile, split, r) + 4 * c) = v;
+      else
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + row_at(a, b, h, r0 + r).o + 8 * c) = v;
     }
     streams_sync();
     if (sbad)
