@@ -179,6 +179,7 @@ struct CacheAttn {
   int quantum;    // a split's keys are a multiple of this
   int PR;         // rows of a split's partial
   int cluster;    // the splits of a tile are a cluster and join by themselves
+  FastDiv by_G, by_Hkv, by_RT, by_S;
   void* ws;       // partial o, then ml
   float2* ml;
 };

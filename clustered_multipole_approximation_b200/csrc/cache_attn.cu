@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
   if (there) s = seq_len(a.c, b);
   cudaGridDependencySynchronize();
   bool live = there && r < s.nn * a.G;
-  const int rt = r / a.rows;
+  const int rt = a.RT == 1 ? 0 : r / a.rows;
   RowTile t{};
   int parts = 1;
   if (live) {
@@ -220,6 +220,10 @@ size_t cache_attn_workspace(const CacheAttn& a0) {
 void run_cache_attn(const CacheAttn& a0, cudaStream_t st) {
   CacheAttn a = a0;
   const Path p = plan(a);
+  a.by_G = fast_div((uint32_t)a.G);
+  a.by_Hkv = fast_div((uint32_t)a.c.Hkv);
+  a.by_RT = fast_div((uint32_t)a.RT);
+  a.by_S = fast_div((uint32_t)a.S);
   const bool join = a.S > 1 && !a.cluster;
   if (join) a.ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(a.ws) + part_bytes(a, false));
   p == kWide ? run_cache_wide(a, st) : p == kStep ? run_cache_step(a, st) : run_cache_chunk(a, st);

@@ -34,7 +34,7 @@ __device__ inline RowTile row_tile(const CacheAttn& a, const SeqLen& s, int r0, 
   RowTile t;
   t.r0 = r0;
   t.r1 = min(s.nn * a.G, r0 + rows);
-  const int2 f = seen(a, s, s.pos0 + r0 / a.G), l = seen(a, s, s.pos0 + (t.r1 - 1) / a.G);
+  const int2 f = seen(a, s, s.pos0 + div_by(a.by_G, r0)), l = seen(a, s, s.pos0 + div_by(a.by_G, max(t.r1 - 1, 0)));
   t.lo = f.x;
   t.hi = max(l.y, f.x);
   t.alo = l.x;
@@ -46,7 +46,7 @@ __host__ __device__ inline int round_up(int x, int m) { return (x + m - 1) / m *
 // Keys of one split of a range of len keys: the call has up to a.S splits for
 // every row tile, a tile uses as many as its own length asks for.
 __device__ inline int split_keys(const CacheAttn& a, int len) {
-  return max(a.minc, round_up((len + a.S - 1) / a.S, a.quantum));
+  return max(a.minc, round_up(div_by(a.by_S, len + a.S - 1), a.quantum));
 }
 __device__ inline int split_count(const CacheAttn& a, int len) {
   const int c = split_keys(a, len);
@@ -63,13 +63,29 @@ __device__ inline float2* part_ml(const CacheAttn& a, long long tile, int split,
   return a.ml + (tile * a.S + split) * a.PR + r;
 }
 
+// The CTA's place in a grid of (sequence, kv-head, row tile, split), the last
+// fastest (fewer than 2^31 CTAs).
+struct Place {
+  int tile, split, rt, b, h;
+};
+__device__ inline Place place_of(const CacheAttn& a) {
+  Place p;
+  p.tile = div_by(a.by_S, (int)blockIdx.x);
+  p.split = (int)blockIdx.x - p.tile * a.S;
+  const int bh = div_by(a.by_RT, p.tile);
+  p.rt = p.tile - bh * a.RT;
+  p.b = div_by(a.by_Hkv, bh);
+  p.h = bh - p.b * a.c.Hkv;
+  return p;
+}
+
 struct RowAt {
   int hq, i;
   long long q, o, lse;  // element offsets
 };
 __device__ inline RowAt row_at(const CacheAttn& a, int b, int h, int r) {
   RowAt x;
-  x.i = r / a.G;
+  x.i = div_by(a.by_G, r);
   x.hq = h * a.G + (r - x.i * a.G);
   x.q = b * a.qs.b + x.hq * a.qs.h + x.i * a.qs.t;
   x.o = b * a.os.b + x.hq * a.os.h + x.i * a.os.t;

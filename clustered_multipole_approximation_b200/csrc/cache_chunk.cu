@@ -225,13 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
   __shared__ int sbad, sfail;
   __shared__ float qback[k8 ? 256 : 1];  // 8-bit: the power of two that undoes a row's factor
 
-  const long long tile = blockIdx.x / a.S;
-  const int split = (int)(blockIdx.x - tile * a.S);
-  const long long bh = tile / a.RT;
-  const int rti = (int)(tile - bh * a.RT);
-  const int b = (int)(bh / a.c.Hkv), h = (int)(bh - (long long)b * a.c.Hkv);
+  const Place at0 = place_of(a);
+  const int tile = at0.tile, split = at0.split, b = at0.b, h = at0.h;
   const SeqLen s = seq_len(a.c, b);
-  const int r0 = rti * 256;
+  const int r0 = at0.rt * 256;
   if (r0 >= s.nn * a.G) return;
   const RowTile rt = row_tile(a, s, r0, 256);
   const int len = rt.hi - rt.lo, parts = split_count(a, len);
@@ -533,12 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tbase + 128 * w + lanes, tO = tbase + 256 + D * w + lanes;
     // what this row, and every row of the stream, sees
-    const int2 see = live ? seen(a, s, s.pos0 + pr / a.G) : make_int2(0, 0);
+    const int2 see = live ? seen(a, s, s.pos0 + div_by(a.by_G, pr)) : make_int2(0, 0);
     int alo = rt.alo, ahi = rt.ahi;
     if (two) {
       const int f = r0 + 128 * w, e = min(rt.r1, f + 128) - 1;
-      alo = seen(a, s, s.pos0 + e / a.G).x;
-      ahi = seen(a, s, s.pos0 + f / a.G).y;
+      alo = seen(a, s, s.pos0 + div_by(a.by_G, e)).x;
+      ahi = seen(a, s, s.pos0 + div_by(a.by_G, f)).y;
     }
     const float sl2 = a.scale * kLog2e * (k8 ? qback[two ? 128 * w + row : row] : 1.f);
     const bool pos = a.scale > 0.f;
@@ -756,14 +753,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     streams_sync();
     // whole rows from there: a lane's own row to global memory would touch 32 lines
     // a store (up to 8000 cycles a tile, 16 % of it)
-    const int pieces = (parts > 1 ? 4 : 2) * D / 16;
-    for (int e = tid; e < (rt.r1 - r0) * pieces; e += 256) {
-      const int r = e / pieces, c = e - r * pieces;
-      const uint4 v = *reinterpret_cast<const uint4*>(rows_sm + r * pitch + 16 * c);
-      if (parts > 1)
-        *reinterpret_cast<uint4*>(part_o<D>(a, tile, split, r) + 4 * c) = v;
-      else
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + row_at(a, b, h, r0 + r).o + 8 * c) = v;
+    if (parts > 1) {
+      constexpr int P = D / 4;
+      const int c = tid % P;
+      for (int r = tid / P; r < rt.r1 - r0; r += 256 / P)
+        *reinterpret_cast<uint4*>(part_o<D>(a, tile, split, r) + 4 * c) =
+            *reinterpret_cast<const uint4*>(rows_sm + r * pitch + 16 * c);
+    } else {
+      constexpr int P = D / 8;
+      const int c = tid % P;
+      for (int r = tid / P; r < rt.r1 - r0; r += 256 / P)
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + row_at(a, b, h, r0 + r).o + 8 * c) =
+            *reinterpret_cast<const uint4*>(rows_sm + r * pitch + 16 * c);
     }
     streams_sync();
     if (sbad)

@@ -90,9 +90,8 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
   extern __shared__ __align__(128) unsigned char step_sm[];
   __shared__ float qback[L::ROWS];  // 8-bit: the power of two that undoes a row's factor
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const long long tile = blockIdx.x / a.S;
-  const int split = (int)(blockIdx.x - tile * a.S);
-  const int b = (int)(tile / a.c.Hkv), h = (int)(tile - (long long)b * a.c.Hkv);
+  const Place at0 = place_of(a);
+  const int tile = at0.tile, split = at0.split, b = at0.b, h = at0.h;
   const SeqLen s = seq_len(a.c, b);
   if (s.nn == 0) return;
   const RowTile rt = row_tile(a, s, 0, L::ROWS);
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_step_kernel(const __grid_co
 #pragma unroll
     for (int e = 0; e < HR; ++e) {
       const int r = 16 * i + 8 * e + g;
-      see[i][e] = seen(a, s, s.pos0 + r / a.G);
+      see[i][e] = seen(a, s, s.pos0 + div_by(a.by_G, r));
       see[i][e].y = min(see[i][e].y, t1);
       mul[i][e] = a.scale * kLog2e * (k8 ? qback[r] : 1.f);
     }

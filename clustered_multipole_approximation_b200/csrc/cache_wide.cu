@@ -98,11 +98,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) cache_wide_kernel(const 
   constexpr int WN = 128 / R, NS = kBlock / 8 / WN, NO = D / 8 / WN;
   constexpr int LPR = D / 8, PASS = 256 / LPR, NP = kBlock / PASS;
   extern __shared__ __align__(16) float wide_sm[];
-  const long long tile = blockIdx.x / a.S;
-  const int split = (int)(blockIdx.x - tile * a.S);
-  const long long bh = tile / a.RT;
-  const int r0 = (int)(tile - bh * a.RT) * R;
-  const int b = (int)(bh / a.c.Hkv), h = (int)(bh - (long long)b * a.c.Hkv);
+  const Place at0 = place_of(a);
+  const int tile = at0.tile, split = at0.split, b = at0.b, h = at0.h, r0 = at0.rt * R;
   const SeqLen s = seq_len(a.c, b);
   if (r0 >= s.nn * a.G) return;
   const RowTile rt = row_tile(a, s, r0, R);
@@ -143,7 +140,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) cache_wide_kernel(const 
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int r = r0 + y * RT + i;
-    see[i] = r < rt.r1 ? seen(a, s, s.pos0 + r / a.G) : make_int2(0, 0);
+    see[i] = r < rt.r1 ? seen(a, s, s.pos0 + div_by(a.by_G, r)) : make_int2(0, 0);
     see[i].y = min(see[i].y, t1);
     m[i] = kFloor;
     l[i] = 0.f;
