@@ -149,12 +149,16 @@ Path plan_keys(CacheAttn& a, long long cap) {
     }
     a.minc = 64;
   } else if (p == kStep) {
-    // keys of a split: enough splits for eight CTAs an SM, none of more than
-    // 512 KB of cache, and no more than 128 a row
+    // Keys of a split.  Enough for eight CTAs an SM; but, as long as two an SM are
+    // left, 256 KB of cache, which pays for a CTA's start (37 x 8 kv-heads of 128 at
+    // 1265 in e4m3: one split 25 us, two 39); and 512 KB at most, for the tail.
     const int size = a.type == kCacheBf16 ? 2 : 1;
+    const long long bytes = 2 * a.c.D * size, most = quanta((512 << 10) / bytes);
     long long c = quanta(cap * units / (kSMs * 8) + 1);
-    const long long most = quanta((512 << 10) / (2 * a.c.D * size));
+    const long long some = quanta((256 << 10) / bytes), two = quanta(cap * units / (kSMs * 2) + 1);
+    if (c < some && c < two) c = some < two ? some : two;
     if (c > most) c = most;
+    if (units >= 2 * kSMs && cap <= most) c = quanta(cap);  // one split, no join
     if (c * 128 < cap) c = quanta((cap + 127) / 128);
     // (and no more than 64 CTAs an SM in all: workspace for nothing)
     if (c * (kSMs * 64) < cap * units) c = quanta(cap * units / (kSMs * 64));
@@ -163,8 +167,13 @@ Path plan_keys(CacheAttn& a, long long cap) {
     // a table far wider than its sequences: shorter splits while few rows fill the SMs
     const long long least = quanta(c * units / (2 * kSMs));
     a.minc = (int)(least < c ? least : c);
-    if (a.S > 1 && a.S <= 16) {  // up to eight join without a second launch
-      a.S = a.S < 8 ? a.S : 8;
+    // Up to eight splits join as a cluster, without a second launch -- where the
+    // grid fits the SMs at once: one token of 8 heads at 1000 8 us against 11, but
+    // clusters that wait for one another's places took 485 us where 64 sequences of
+    // 16384 take 389.
+    const int S8 = a.S < 8 ? a.S : 8;
+    if (a.S > 1 && units * S8 <= 2 * kSMs && (a.S <= 8 || cap <= 8 * 512)) {
+      a.S = S8;
       a.cluster = 1;
     }
   } else {
