@@ -168,7 +168,9 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(Cache c, const T*
   put<CT, LPR>(c.v, c.vs, row, D, col, row >= 0, y);
 }
 
-// Work item: (sequence, head, row of the output), the output's own order.
+// Work item: (sequence, head, row of the output), the output's own order.  (Two
+// rows a lane put more bytes behind the chain length, page, row, but took the
+// registers of half the warps: 59 us against 42.)
 template <typename T, int CT, int D>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(Cache c, T* K, T* V, const int* start,
                                                               int N, int rows, FastDiv heads,

@@ -88,15 +88,11 @@ __device__ inline long long row_of(const Cache& c, int b, int h, int pos) {
   return ((long long)pg * c.Hkv + h) * c.page.d + (pos - p * (int)c.page.d);
 }
 
-// Two values of the 8-bit types held in the low 16 bits of x.
+// Two e4m3 values held in the low 16 bits of x.
 __device__ inline float2 e4m3x2(uint32_t x) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xFFFF), __NV_E4M3);
   return __half22float2(__half2(h));
 }
-__device__ inline float2 i8x2(uint32_t x) {
-  return make_float2((float)(int8_t)(x & 0xFF), (float)(int8_t)((x >> 8) & 0xFF));
-}
-
 // Eight consecutive values of row `row`, columns [8 c, 8 c + 8), in fp32 (with
 // the row's scale where the cache has one).  row < 0: zeros.
 template <int CT>
@@ -124,12 +120,21 @@ __device__ inline void load8(const void* base, const float* scales, long long ro
   } else {
     const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(base) + at);
     const float s = scales[row];
-    const uint32_t v[4] = {w.x, w.x >> 16, w.y, w.y >> 16};
+    if (CT == kCacheE4m3) {
+      const uint32_t v[4] = {w.x, w.x >> 16, w.y, w.y >> 16};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = CT == kCacheE4m3 ? e4m3x2(v[e]) : i8x2(v[e]);
-      x[2 * e] = f.x * s;
-      x[2 * e + 1] = f.y * s;
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = e4m3x2(v[e]);
+        x[2 * e] = f.x * s;
+        x[2 * e + 1] = f.y * s;
+      }
+    } else {
+      // q + 128 in the last bits of 2^23 (a conversion instruction takes four times
+      // as long)
+      const uint32_t v[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = (__uint_as_float(__byte_perm(v[e >> 2], 0x4B000000u, 0x7440 | (e & 3))) - 8388736.f) * s;
     }
   }
 }
