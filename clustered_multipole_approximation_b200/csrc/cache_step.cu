@@ -23,11 +23,11 @@
 // more leave partials for cache_join_kernel.
 //
 // Measured: 64 sequences of up to 16384 tokens, 32 heads over 8 of 128, bf16:
-// 468 us, 5.5 TB/s of cache (84 % of a copy's rate).  8 sequences of up to 65536
-// of 64 in e4m3: 92 us, 61 %: conversions and masks fill the integer pipe.  Five
-// tokens each (20 rows) over int8 of 128: 75 us, 23 %: two row tiles leave two
-// warps a scheduler, whose latencies bound it.  One token at 1000: 8.2 us, the
-// chain launch, lengths, pages, rows, join.
+// 389 us, 6.6 TB/s of cache, a copy's rate.  8 sequences of up to 65536 of 64 in
+// e4m3: 92 us, 61 %: conversions and masks fill the integer pipe.  Five tokens
+// each (20 rows) over int8 of 128: 66 us, 26 %: two row tiles leave two warps a
+// scheduler, whose latencies bound it.  One token at 1000: 8.2 us, the chain
+// launch, lengths, pages, rows, join.
 #include <cooperative_groups.h>
 
 #include "cache_attn.cuh"

@@ -10,10 +10,11 @@
 // than the additions in fp32 lose over D = 64 terms.  The softmax between them
 // is a thread's R / 16 rows and every 16th key, row statistics by shuffles,
 // weights through shared memory.
-// Two sequences of 130 tokens at 2100, 8 heads over 2 of 64: 46 us, of which the
-// kernel takes 40 (tensor cores 26 % busy; the splitting's integer operations
+// Two sequences of 130 tokens at 2100, 8 heads over 2 of 64: 40 us, of which the
+// kernel takes 34 (tensor cores 28 % busy; the splitting's integer operations
 // and the four barriers of a block bound it).  The same tile as fp32 FMAs was
-// bound by shared memory's reads: 49 us, and 58 against 46 for single tokens.
+// bound by shared memory's reads: 4 us more, and 58 us against 46 for single
+// tokens over int8.
 //
 // An infinity has no such split (nor has the last step below one): a CTA that
 // meets a value that is not finite forms its rows again key by key (redo_row).
