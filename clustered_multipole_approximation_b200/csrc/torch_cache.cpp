@@ -207,6 +207,8 @@ PyObject* guarded(const char* name, Py_ssize_t n, Py_ssize_t want, F&& body) {
     Py_XDECREF(torch);
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
   }
   return nullptr;
 }
