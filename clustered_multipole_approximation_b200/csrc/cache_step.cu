@@ -24,7 +24,7 @@
 //
 // Measured: 64 sequences of up to 16384 tokens, 32 heads over 8 of 128, bf16:
 // 389 us, 6.6 TB/s of cache, a copy's rate.  8 sequences of up to 65536 of 64 in
-// e4m3: 92 us, 61 %: conversions and masks fill the integer pipe.  Five tokens
+// e4m3: 89 us, 63 %: conversions and masks fill the integer pipe.  Five tokens
 // each (20 rows) over int8 of 128: 66 us, 26 %: two row tiles leave two warps a
 // scheduler, whose latencies bound it.  One token at 1000: 8.2 us, the chain
 // launch, lengths, pages, rows, join.
@@ -49,9 +49,10 @@ struct StepL {
   static constexpr int HALF = KB * RB;               // K (or V) of a block
   static constexpr int SCALES = SZ == 1 ? 2 * KB * 4 : 0;
   static constexpr int STAGE = 2 * HALF + SCALES;
-  // stages of a warp's ring: at 8 bits of 128 two, so that three CTAs fit an SM
-  // (16 heads of 33147 rows, e4m3, 5 ragged sequences: 93 -> 82 us)
-  static constexpr int NS = SZ == 1 && D == 128 && MT == 1 ? 2 : 3;
+  // stages of a warp's ring: two for 8-bit rows, so that one more CTA fits an SM
+  // (5 ragged sequences of up to 33147, 16 heads of 128, e4m3: 93 -> 82 us; 26 of
+  // 18349, 16 of 64: 236 -> 224)
+  static constexpr int NS = SZ == 1 && MT == 1 ? 2 : 3;
   static constexpr int RING = NS * STAGE;
   static constexpr int ROWS = 16 * MT;
   static constexpr int JOIN = ROWS * D * 4 + ROWS * 8;  // o, (m, l) of a warp
