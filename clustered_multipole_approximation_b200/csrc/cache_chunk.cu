@@ -548,11 +548,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       const int T = tile_at(w, k), tb = t0 + T * kKeys;
       wait(mS[w], k);
       fence_after();
+      const int vi = v_item(T);
+      if (CT != kCacheI8 && (tb < alo || tb + kKeys > ahi)) {
+        // values that are not numbers would reach the rows that do not see them; every
+        // warp of the stream looks through its keys, one without rows too
+        wait(mFull[vi % NS], vi / NS);
+        constexpr int P = D / 8, RP = 128 / P;  // pieces of a key, keys of a pass
+        const int c = row % P;
+        const unsigned char* sv = sm + L::STAGES + (vi % NS) * L::SS + (c >> 3) * L::QC;
+        uint32_t f = 0;  // a half's upper bit: its exponent is all ones
+#pragma unroll 8
+        for (int r = row / P; r < kKeys; r += RP) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sv + swz(r, c & 7));
+          const uint32_t z = ((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
+                             ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u);
+          f |= tb + r >= alo && tb + r < ahi ? 0 : z;  // (a key that every row sees may be anything)
+        }
+        if (f & 0x80008000u) sbad = 1;
+      }
       if (idle) {  // no row of this warp is used, whatever its P is
+        __syncwarp();
         if (lane < 2) mbar_arrive(smem_u32(&mP[w][lane]));
         continue;
       }
-      const int vi = v_item(T);
       const float* sc = reinterpret_cast<const float*>(sm + L::SC) + (T % kScales) * 2 * kKeys;
       const bool edge = tb < alo || tb + kKeys > ahi || tb + kKeys > t1;
       const int clo = see.x - tb, chi = min(see.y, t1) - tb;
@@ -629,22 +647,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       for (int q = 0; q < 4; ++q) tld32(tS + 32 * q, x + 32 * q);
 #pragma unroll
       for (int q = 0; q < 4; ++q) tld_wait(x + 32 * q);
-      if (CT != kCacheI8 && (tb < alo || tb + kKeys > ahi)) {
-        // values that are not numbers would reach the rows that do not see them
-        wait(mFull[vi % NS], vi / NS);
-        constexpr int P = D / 8, RP = 128 / P;  // pieces of a key, keys of a pass
-        const int c = row % P;
-        const unsigned char* sv = sm + L::STAGES + (vi % NS) * L::SS + (c >> 3) * L::QC;
-        uint32_t f = 0;  // a half's upper bit: its exponent is all ones
-#pragma unroll 8
-        for (int r = row / P; r < kKeys; r += RP) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sv + swz(r, c & 7));
-          const uint32_t z = ((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
-                             ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u);
-          f |= tb + r >= alo && tb + r < ahi ? 0 : z;  // (a key that every row sees may be anything)
-        }
-        if (f & 0x80008000u) sbad = 1;
-      }
       logits(0);
       logits(64);
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

@@ -1,0 +1,47 @@
+"""The paged-cache operators at the edges of their tiles: values that are not
+numbers in every place of a tile, and scales and rows at the ends of the range."""
+import numpy as np
+import pytest
+import torch
+
+import clustered_multipole_approximation_b200 as muse
+from clustered_multipole_approximation_b200 import build
+from cache_ref import Paged, attend
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return muse.load_library()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 9])
+@pytest.mark.parametrize("n,Hq", [(33, 1), (70, 1), (20, 2), (130, 1), (50, 3), (5, 2)])
+def test_a_value_that_is_not_a_number_in_every_place(n, Hq, window, D, cache):
+    """Row counts that leave softmax warps without a row, the value at each of 16
+    neighbouring positions: rows that do not see it are as if it were not there."""
+    kv = n + 90
+    P = Paged(1, 1, D, [kv], 16, cache)
+    q = torch.randn(1, Hq, n, D, generator=torch.Generator().manual_seed(4)).bfloat16()
+    scale = D ** -0.5
+    ro, _, to, _ = attend(P, q, [n], scale, window=window)
+    c = P.gpu()
+    pos = kv - n + np.arange(n)
+    for at in range(kv - 17, kv):
+        pg, r = P.where(0, at)
+        keep = c["v_cache"].clone()
+        c["v_cache"].view(torch.uint8 if cache == "e4m3" else torch.int16)[pg, :, r, 5] = \
+            0x7F if cache == "e4m3" else 0x7FC0
+        o = muse.muse_attn_cache(q.cuda(), **c, scale=scale, window=window).double().cpu().numpy()
+        c["v_cache"] = keep
+        sees = (at <= pos) & ((at > pos - window) if window else True)
+        assert np.isnan(o[:, :, sees, 5]).all(), at
+        fine = np.ones(o.shape, bool)
+        fine[:, :, sees, 5] = False
+        bad = fine & ~(np.abs(o - ro) <= to)
+        bad[:, :, sees] = False  # (their other columns: the split-call tests)
+        assert not bad.any(), (at, np.argwhere(bad)[:4])
