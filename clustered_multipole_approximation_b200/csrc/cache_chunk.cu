@@ -538,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       ahi = seen(a, s, s.pos0 + div_by(a.by_G, f)).y;
     }
     const float sl2 = a.scale * kLog2e * (k8 ? qback[two ? 128 * w + row : row] : 1.f);
-    const bool pos = a.scale > 0.f;
+    // (not the scale's sign: a product of small factors may be zero, and 0 x -inf is no mask)
+    const bool pos = sl2 > 0.f;
     const float mul = pos ? sl2 : 1.f;
     const uint64_t mul2x = twice(mul);
     float m = kFloor, l = 0.f;

@@ -7,6 +7,7 @@ import torch
 import clustered_multipole_approximation_b200 as muse
 from clustered_multipole_approximation_b200 import build
 from cache_ref import Paged, attend
+from test_gpu_cache import run_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,15 @@ def test_a_value_that_is_not_a_number_in_every_place(n, Hq, window, D, cache):
         bad = fine & ~(np.abs(o - ro) <= to)
         bad[:, :, sees] = False  # (their other columns: the split-call tests)
         assert not bad.any(), (at, np.argwhere(bad)[:4])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("n", [1, 9, 40, 150])
+@pytest.mark.parametrize("scale", [2.0 ** -148, 1e-20])
+def test_scales_and_rows_next_to_zero(n, scale, cache):
+    """The factor that undoes a row's power of two, times the scale, is zero in
+    fp32: the weights are equal, and masked keys stay out."""
+    q = torch.randn(1, 2, n, 64, generator=torch.Generator().manual_seed(6))
+    q[:, :, 0::3] = 0.0
+    q[:, :, 1::3] *= 1e-30
+    run_attend(Paged(1, 1, 64, [n + 200], 16, cache), n, [n], 2, scale=scale, q=q.bfloat16())
