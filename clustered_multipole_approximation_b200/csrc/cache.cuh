@@ -35,8 +35,12 @@ inline FastDiv fast_div(uint32_t d) {
   }
   return f;
 }
-__device__ inline int div_by(const FastDiv& f, int n) {
+__host__ __device__ inline int div_by(const FastDiv& f, int n) {
+#ifdef __CUDA_ARCH__
   return f.d == 1 ? n : (int)(__umulhi((uint32_t)n, f.mul) >> f.shift);
+#else
+  return f.d == 1 ? n : (int)((uint32_t)((uint64_t)(uint32_t)n * f.mul >> 32) >> f.shift);
+#endif
 }
 
 struct Strides {  // elements
@@ -199,6 +203,9 @@ void run_cache_write(const Cache& c, int type, const void* K, const void* V, con
 void run_cache_read(const Cache& c, int type, void* K, void* V, int f32, int B, int N,
                     const int* start, cudaStream_t st);
 size_t cache_attn_workspace(const CacheAttn& a);
+// The division of the call's keys (a's fields), and what a row tile that sees
+// `len` of them makes of it.
+void cache_attn_division(CacheAttn& a, int len, int* parts, int* keys);
 void run_cache_attn(const CacheAttn& a, cudaStream_t st);
 
 }  // namespace muse

@@ -173,6 +173,25 @@ size_t muse_attn_cache_workspace_size(const muse_shape* sh, const muse_cache* ca
   return cache_attn_workspace(attn_args(sh, ca, ix, nullptr));
 }
 
+muse_status muse_debug_cache_division(const muse_shape* sh, const muse_cache* ca,
+                                      const muse_cache_index* ix, int window, int len,
+                                      muse_cache_division* out) {
+  muse_status s = check_shape(sh);
+  if (s == MUSE_OK) s = check_cache(ca, ix, sh->Hkv);
+  if (s != MUSE_OK) return s;
+  if (!out || window < 0 || len < 0 || len > ix->wide * ca->page_size)
+    return fail(MUSE_ERR_INVALID_ARG, "out must not be NULL, window >= 0 and len within the table");
+  CacheAttn a = attn_args(sh, ca, ix, nullptr);
+  a.window = window >= 1 << 30 ? 0 : window;
+  cache_attn_division(a, len, &out->parts, &out->keys);
+  out->tiles = (long long)sh->B * sh->Hkv * a.RT;
+  out->rows = a.PR;
+  out->splits = a.S;
+  out->cluster = a.cluster;
+  out->quantum = a.quantum;
+  return MUSE_OK;
+}
+
 muse_status muse_attn_cache(const void* Q, const muse_strides* qs, void* O, const muse_strides* os,
                             float* lse, const muse_shape* sh, const muse_cache* ca,
                             const muse_cache_index* ix, float scale, int causal, int window,

@@ -166,7 +166,9 @@ Path plan_keys(CacheAttn& a, long long cap) {
     while (a.S > 1 && units * a.S > 0x7FFFFFFF) a.S = (a.S + 1) / 2;  // the grid
     // a table far wider than its sequences: shorter splits while few rows fill the SMs
     const long long least = quanta(c * units / (2 * kSMs));
+    // (but a quantum at least: a row tile that sees nothing divides by it too)
     a.minc = (int)(least < c ? least : c);
+    if (a.minc < kQuantum) a.minc = kQuantum;
     // Up to eight splits join as a cluster, without a second launch -- where the
     // grid fits the SMs at once: one token of 8 heads at 1000 8 us against 11, but
     // clusters that wait for one another's places took 485 us where 64 sequences of
@@ -224,6 +226,13 @@ size_t cache_attn_workspace(const CacheAttn& a0) {
   CacheAttn a = a0;
   plan(a);
   return a.S > 1 && !a.cluster ? part_bytes(a, false) + part_bytes(a, true) : 256;
+}
+
+void cache_attn_division(CacheAttn& a, int len, int* parts, int* keys) {
+  plan(a);
+  a.by_S = fast_div((uint32_t)a.S);
+  *keys = split_keys(a, len);
+  *parts = *keys > 0 ? split_count(a, len) : 0;
 }
 
 void run_cache_attn(const CacheAttn& a0, cudaStream_t st) {

@@ -45,12 +45,13 @@ __host__ __device__ inline int round_up(int x, int m) { return (x + m - 1) / m *
 
 // Keys of one split of a range of len keys: the call has up to a.S splits for
 // every row tile, a tile uses as many as its own length asks for.
-__device__ inline int split_keys(const CacheAttn& a, int len) {
-  return max(a.minc, round_up(div_by(a.by_S, len + a.S - 1), a.quantum));
+__host__ __device__ inline int split_keys(const CacheAttn& a, int len) {
+  const int keys = round_up(div_by(a.by_S, len + a.S - 1), a.quantum);
+  return keys > a.minc ? keys : a.minc;
 }
-__device__ inline int split_count(const CacheAttn& a, int len) {
-  const int c = split_keys(a, len);
-  return max(1, (len + c - 1) / c);
+__host__ __device__ inline int split_count(const CacheAttn& a, int len) {
+  const int c = split_keys(a, len), n = (len + c - 1) / c;  // c >= minc >= 1
+  return n > 1 ? n : 1;
 }
 
 // Split partials in the workspace: o (relative to 2^m, not divided by l), m, l

@@ -48,6 +48,11 @@ class muse_strides(ctypes.Structure):
     _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("t", ctypes.c_int64)]
 
 
+class muse_cache_division(ctypes.Structure):
+    _fields_ = [("tiles", ctypes.c_longlong)] + [
+        (x, ctypes.c_int) for x in ("rows", "splits", "cluster", "quantum", "parts", "keys")]
+
+
 def declare(lib) -> None:
     """Signatures of the cache entry points."""
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
@@ -59,6 +64,8 @@ def declare(lib) -> None:
     lib.muse_cache_read.argtypes = [vp, vp, sh, ca, ix, vp, vp, vp]
     lib.muse_attn_cache_workspace_size.restype = sz
     lib.muse_attn_cache_workspace_size.argtypes = [sh, ca, ix]
+    lib.muse_debug_cache_division.restype = i32
+    lib.muse_debug_cache_division.argtypes = [sh, ca, ix, i32, i32, ctypes.POINTER(muse_cache_division)]
     lib.muse_attn_cache.restype = i32
     lib.muse_attn_cache.argtypes = [vp, st, vp, st, vp, sh, ca, ix, ctypes.c_float, i32, i32, vp,
                                     vp, sz, vp]

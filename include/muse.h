@@ -486,6 +486,19 @@ int muse_profile_read(char *names, int name_stride, int *launches, double *ms,
  * thread-safe. */
 void muse_debug_inject_barrier_fault(int rank, int spin_limit);
 
+/* How muse_attn_cache divides its keys, for tests (host arithmetic; no pointer
+ * is read): `tiles` row tiles of up to `rows` packed rows, `splits` CTAs each,
+ * which join as a cluster or (splits > 1, cluster == 0) through the workspace;
+ * a row tile that sees `len` keys uses `parts` of its splits, of `keys` keys
+ * each (a multiple of `quantum`). */
+typedef struct {
+  long long tiles;
+  int rows, splits, cluster, quantum, parts, keys;
+} muse_cache_division;
+muse_status muse_debug_cache_division(const muse_shape *shape, const muse_cache *cache,
+                                      const muse_cache_index *index, int window, int len,
+                                      muse_cache_division *out);
+
 /* Message of the last failing call on this host thread ("" if none). */
 const char *muse_last_error(void);
 

@@ -1,0 +1,58 @@
+"""How the attention over the paged cache divides its keys, on the host: every
+row tile, of whatever length, gets splits that hold its keys and that the grid,
+the cluster and the workspace have room for."""
+import itertools
+
+import pytest
+
+import clustered_multipole_approximation_b200 as muse
+from clustered_multipole_approximation_b200 import build
+from clustered_multipole_approximation_b200.kv_cache import muse_cache, muse_cache_division, muse_cache_index
+
+FAKE = 0x1000  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return muse.load_library()
+
+
+def lengths(cap):
+    some = {0, 1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 512, 513, cap // 3, cap // 2, cap - 1, cap}
+    return sorted(x for x in some if 0 <= x <= cap)
+
+
+@pytest.mark.parametrize("dtype,cache", [(0, 0), (0, 2), (0, 3), (0, 1), (1, 1), (1, 0), (1, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_length_has_its_splits(lib, dtype, cache, D):
+    scale = FAKE if cache >= 2 else None
+    for (B, Hkv), G, n, (page, wide), window in itertools.product(
+            [(1, 1), (1, 2), (2, 1), (1, 8), (3, 5), (64, 8), (40, 16)], [1, 3, 8], [1, 5, 40, 300, 2048],
+            [(1, 1), (16, 2), (16, 64), (24, 100), (16, 1024), (256, 256), (64, 1 << 14), (1024, 1 << 20)],
+            [0, 1, 300, 5000, 1 << 30]):
+        sh = muse.muse_shape(B, Hkv * G, Hkv, n, D, dtype, 0)
+        ca = muse_cache(FAKE, FAKE, scale, scale, 64, page, cache)
+        ix = muse_cache_index(FAKE, FAKE, None, wide)
+        size = lib.muse_attn_cache_workspace_size(sh, ca, ix)
+        assert size > 0
+        what = (B, Hkv, G, n, page, wide, window)
+        for length in lengths(page * wide):
+            d = muse_cache_division()
+            assert lib.muse_debug_cache_division(sh, ca, ix, window, length, d) == 0
+            assert d.keys > 0 and d.keys % d.quantum == 0, what
+            assert 1 <= d.parts <= d.splits and d.tiles * d.splits < 1 << 31, what
+            assert d.parts * d.keys >= length and (d.parts == 1 or (d.parts - 1) * d.keys < length), what
+            if d.splits > 1 and not d.cluster:  # partial rows, maxima and sums
+                assert size >= d.tiles * d.splits * d.rows * (D * 4 + 8), what
+            assert not d.cluster or d.splits <= 8, what
+
+
+def test_refusals(lib):
+    sh, ca, ix = muse.muse_shape(1, 1, 1, 1, 64, 0, 0), muse_cache(FAKE, FAKE, None, None, 4, 16, 0), \
+        muse_cache_index(FAKE, FAKE, None, 2)
+    d = muse_cache_division()
+    f = lib.muse_debug_cache_division
+    assert f(sh, ca, ix, 0, 32, d) == 0
+    assert f(sh, ca, ix, 0, 33, d) == 1 and f(sh, ca, ix, 0, -1, d) == 1 and f(sh, ca, ix, -1, 1, d) == 1
+    assert f(sh, ca, ix, 0, 1, None) == 1 and f(None, ca, ix, 0, 1, d) == 1

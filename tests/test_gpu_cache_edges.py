@@ -58,3 +58,16 @@ def test_scales_and_rows_next_to_zero(n, scale, cache):
     q[:, :, 0::3] = 0.0
     q[:, :, 1::3] *= 1e-30
     run_attend(Paged(1, 1, 64, [n + 200], 16, cache), n, [n], 2, scale=scale, q=q.bfloat16())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "i8", "f32"])
+@pytest.mark.parametrize("B,Hkv", [(1, 1), (1, 2), (2, 1)])
+@pytest.mark.parametrize("wide", [64, 1024])
+@pytest.mark.parametrize("n", [1, 3])
+def test_row_tiles_that_see_nothing_in_divided_calls(n, wide, B, Hkv, cache):
+    """Tables of 1024 (splits that join in a cluster) and 16384 positions (through
+    the workspace), no token cached, alone and beside a long sequence."""
+    for kv in ([0] * B, [700] * (B - 1) + [0], [n - 1] * B):
+        P = Paged(B, Hkv, 64, kv, 16, cache, wide=wide)
+        for causal in (True, False):
+            run_attend(P, n, [n] * B, 4 * Hkv, causal=causal)
