@@ -69,7 +69,8 @@ EXPORTS = ["muse_workspace_size", "muse_cluster_workspace_size", "muse_cluster",
            "muse_attn_bwd_workspace_size", "muse_attn_bwd", "muse_accum_workspace_size",
            "muse_attn_fwd_causal_accum", "muse_attn_bwd_causal_workspace_size",
            "muse_attn_bwd_causal", "muse_cache_write", "muse_cache_read",
-           "muse_attn_cache_workspace_size", "muse_attn_cache", "muse_debug_cache_division"]
+           "muse_attn_cache_workspace_size", "muse_attn_cache", "muse_debug_cache_division",
+           "muse_debug_inject_cache_fault"]
 
 # Bits of the device error word (include/muse.h MUSE_DEVERR_*).
 DEVERR = {1: "MUSE_DEVERR_MMA_WAIT", 2: "MUSE_DEVERR_TEAM_BARRIER", 4: "MUSE_DEVERR_V_RANGE",

@@ -189,6 +189,7 @@ struct CacheAttn {
   int PR;         // rows of a split's partial
   int cluster;    // the splits of a tile are a cluster and join by themselves
   FastDiv by_G, by_Hkv, by_RT, by_S;
+  int lost;       // failure tests: this load of every chunk CTA is never reported (-1: none)
   void* ws;       // partial o, then ml
   float2* ml;
 };
@@ -207,5 +208,6 @@ size_t cache_attn_workspace(const CacheAttn& a);
 // `len` of them makes of it.
 void cache_attn_division(CacheAttn& a, int len, int* parts, int* keys);
 void run_cache_attn(const CacheAttn& a, cudaStream_t st);
+void set_cache_fault(int load);
 
 }  // namespace muse

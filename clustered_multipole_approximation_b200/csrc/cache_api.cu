@@ -173,6 +173,8 @@ size_t muse_attn_cache_workspace_size(const muse_shape* sh, const muse_cache* ca
   return cache_attn_workspace(attn_args(sh, ca, ix, nullptr));
 }
 
+void muse_debug_inject_cache_fault(int load) { set_cache_fault(load < 0 ? -1 : load); }
+
 muse_status muse_debug_cache_division(const muse_shape* sh, const muse_cache* ca,
                                       const muse_cache_index* ix, int window, int len,
                                       muse_cache_division* out) {

@@ -112,6 +112,9 @@ void run_join(const CacheAttn& a, cudaStream_t st) {
   a.c.D == 64 ? join_of<T, 64>(a, st) : join_of<T, 128>(a, st);
 }
 
+// Failure-path testing (muse_debug_inject_cache_fault).
+int g_lost_load = -1;
+
 enum Path { kWide, kStep, kChunk };
 Path path_of(const CacheAttn& a) {
   if (a.f32 || a.type == kCacheF32) return kWide;
@@ -235,6 +238,8 @@ void cache_attn_division(CacheAttn& a, int len, int* parts, int* keys) {
   *parts = *keys > 0 ? split_count(a, len) : 0;
 }
 
+void set_cache_fault(int load) { g_lost_load = load; }
+
 void run_cache_attn(const CacheAttn& a0, cudaStream_t st) {
   CacheAttn a = a0;
   const Path p = plan(a);
@@ -242,6 +247,7 @@ void run_cache_attn(const CacheAttn& a0, cudaStream_t st) {
   a.by_Hkv = fast_div((uint32_t)a.c.Hkv);
   a.by_RT = fast_div((uint32_t)a.RT);
   a.by_S = fast_div((uint32_t)a.S);
+  a.lost = g_lost_load;
   const bool join = a.S > 1 && !a.cluster;
   if (join) a.ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(a.ws) + part_bytes(a, false));
   p == kWide ? run_cache_wide(a, st) : p == kStep ? run_cache_step(a, st) : run_cache_chunk(a, st);

@@ -24,7 +24,9 @@
 // Warps 0-7: softmax of stream 0 (0-3) and 1 (4-7); 8-11: loads; 12: products.
 // One warp issues all products, the streams in turn: that keeps them half a
 // step apart (two issuing warps drift into step, softmax against softmax).
-// Every wait is bounded; one that gives up sets kErrMmaWait.
+// Every wait is bounded.  After one that gives up each role leaves its loop: no
+// further copies, products or reports; copies and products on their way are
+// waited for before the CTA ends, the rows are NaN and kErrMmaWait is set.
 //
 // What bounds it: a stream's chain S -> maximum -> exponentials -> P V -> S,
 // about 3300 cycles a tile pair at D = 128 where the products alone take 2100.
@@ -194,6 +196,17 @@ __device__ inline void fence_before() { asm volatile("tcgen05.fence::before_thre
 __device__ inline void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ inline void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 __device__ inline void streams_sync() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
+// The same barrier; whether any of its threads says so.
+__device__ inline bool streams_any(bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, 1, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(y)
+      : "r"((uint32_t)x)
+      : "memory");
+  return y != 0;
+}
 
 template <int CT, int D>
 struct ChunkL {
@@ -220,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
   extern __shared__ __align__(1024) unsigned char chunk_raw[];
   unsigned char* sm = chunk_raw + ((1024 - (smem_u32(chunk_raw) & 1023)) & 1023);
   const uint32_t sb = smem_u32(sm);
-  __shared__ __align__(8) uint64_t mFull[NS], mEmpty[NS], mS[2], mP[2][2], mO[2];
+  __shared__ __align__(8) uint64_t mFull[NS], mEmpty[NS], mS[2], mP[2][2], mO[2], mDone;
   __shared__ uint32_t tslot;
   __shared__ int sbad, sfail;
   __shared__ float qback[k8 ? 256 : 1];  // 8-bit: the power of two that undoes a row's factor
@@ -260,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         mbar_init(smem_u32(&mP[w][1]), 4);
         mbar_init(smem_u32(&mO[w]), 1);
       }
+      mbar_init(smem_u32(&mDone), 1);
       sbad = sfail = 0;
       asm volatile("fence.mbarrier_init.release.cluster;\n");
     }
@@ -306,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
   __syncthreads();
   fence_after();
   const uint32_t tbase = tslot;
-  bool ok = true;
+  bool ok = true;  // this lane's waits; a warp goes on while all its lanes may
+  auto all_ok = [&]() { return __all_sync(0xffffffffu, ok) != 0; };
   auto wait = [&](uint64_t& bar, int use) { ok = ok && mbar_wait(smem_u32(&bar), (uint32_t)(use & 1), &sfail); };
 
   if (warp >= 8 && warp < 12) {
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     auto report = [&](int item) {
       fence_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&mFull[item % NS]));
+      if (lane == 0 && item != a.lost) mbar_arrive(smem_u32(&mFull[item % NS]));
     };
     auto begin = [&](int item) {  // its stage is free
       if (item >= NS) wait(mEmpty[item % NS], item / NS - 1);
@@ -331,6 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         cp_wait<0>();
         report_to(issued);
         begin(item);
+        if (!all_ok()) {
+          ok = false;
+          return;
+        }
       }
       unsigned char* st = sm + L::STAGES + (item % NS) * L::SS;
       constexpr int LPR = D / 8, RPI = 32 / LPR;
@@ -426,12 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           fetch();
           cp_wait<L::RS - 1>();
           begin(item);
+          if (item >= NS && !all_ok()) break;
           if (is_k(item))
             convert(item, std::true_type());
           else
             convert(item, std::false_type());
           report(item);
         }
+        cp_wait<0>();
       } else {
         int rk = first, rv = rk;  // page rows of the next K and the next V
         auto pump = [&]() {
@@ -446,13 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           rk = lookup(T + 1);
           if (T + 1 < nt) {
             copy(k_item(T + 1), a.c.k, rk);
+            if (!ok) break;
             pump();
           }
           copy(v_item(T), a.c.v, rv);
+          if (!ok) break;
           pump();
         }
         cp_wait<0>();
-        report_to(2 * nt);
+        if (ok) report_to(2 * nt);
       }
     }
   } else if (warp >= 12) {
@@ -487,10 +510,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           const int it = k_item(both ? 0 : w);
           wait(mFull[it % NS], it / NS);
           fence_after();
-          issue_s(w, it);
+          if (all_ok()) issue_s(w, it);
         }
 #pragma unroll 1
-      for (int k = 0; k < n0; ++k) {
+      for (int k = 0; k < n0 && all_ok(); ++k) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {  // step k of stream 0, then of stream 1
           const int n = w ? n1 : n0;
@@ -503,10 +526,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
             wait(mFull[vst], vi / NS);
             wait(mFull[ki % NS], ki / NS);
           }
+          bool go = true;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {  // P V of the tile's halves, as P comes
             wait(mP[w][u], k);
             fence_after();
+            go = all_ok();  // the warp's vote: with a lane's own state the products are slower
+            if (!go) break;
             if (elect_one()) {
               const uint64_t bd = vd + vst * (L::SS >> 4);
 #pragma unroll
@@ -517,9 +543,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
             }
             __syncwarp();
           }
-          if (more) issue_s(w, ki);
+          if (more && go) issue_s(w, ki);
         }
       }
+      // what was issued still reads shared memory and writes TMEM and barriers, and after
+      // a wait that gave up no softmax warp waits for its end
+      int late = 0;
+      if (elect_one()) umma_commit(smem_u32(&mDone));
+      __syncwarp();
+      mbar_wait(smem_u32(&mDone), 0, &late);
+      if (late) sfail = 1;
     }
   } else {
     // ---- softmax: thread = row -------------------------------------------------
@@ -569,11 +602,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     const bool idle = !__any_sync(0xffffffffu, live);
     for (int k = 0; idle && k < n; ++k) {  // no row of this warp is used, whatever its P is
       wait(mS[w], k);
+      if (!all_ok()) break;
       look(tile_at(w, k));
       __syncwarp();
       if (lane < 2) mbar_arrive(smem_u32(&mP[w][lane]));
     }
-    for (int k = 0; !idle && k < n; ++k) {
+    for (int k = 0; !idle && k < n && all_ok(); ++k) {
       const int T = tile_at(w, k), tb = t0 + T * kKeys;
       wait(mS[w], k);
       fence_after();
@@ -648,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         tst_wait();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&mP[w][u]));
+        if (lane == 0 && ok) mbar_arrive(smem_u32(&mP[w][u]));
       };
 #pragma unroll
       for (int q = 0; q < 4; ++q) tld32(tS + 32 * q, x + 32 * q);
@@ -699,87 +733,103 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     // then the tile's rows, to be stored line by line
     unsigned char* rows_sm = sm + L::STAGES + (two ? 0 : L::JOIN);
     const int pitch = (parts > 1 ? 4 : 2) * D + 16;
-    streams_sync();  // both streams' products are done
-    if (!two) {
-      if (w == 1 && n > 0) {
+    // Both streams' products are done, and with them all that was loaded -- or a wait
+    // gave up: no numbers, whoever reads the flag.
+    const bool failed = streams_any(!ok);
+    if (failed) {
+      for (int r = warp; r < rt.r1 - r0; r += 8) {
+        const float nan = __int_as_float(0x7FC00000), y[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
+        const RowAt at = row_at(a, b, h, r0 + r);
+        if (lane < D / 8) {
+          if (parts > 1)
+            store8(part_o<D>(a, tile, split, r) + 8 * lane, y);
+          else
+            store8(static_cast<__nv_bfloat16*>(a.O) + at.o + 8 * lane, y);
+        }
+        if (lane == 0 && parts > 1) *part_ml(a, tile, split, r) = make_float2(nan, nan);
+        if (lane == 0 && parts == 1 && a.lse) a.lse[at.lse] = nan;
+      }
+    } else {
+      if (!two) {
+        if (w == 1 && n > 0) {
 #pragma unroll
+          for (int d = 0; d < D; d += 32) {
+            uint32_t r[32];
+            tld32(tO + d, r);
+            tld_wait(r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) jo[(d + e) * 128 + row] = __uint_as_float(r[e]);
+          }
+          jml[row] = make_float2(m, l);
+        }
+        streams_sync();
+      }
+      const bool join = !two && steps(1) > 0;
+      if (two || w == 0) {
+        float f0 = 1.f, f1 = 0.f;
+        if (join) {
+          const float2 ml = jml[row];
+          const float mn = fmaxf(m, ml.x);
+          f0 = fast_exp2(m - mn);
+          f1 = fast_exp2(ml.x - mn);
+          m = mn;
+          l = l * f0 + ml.y * f1;
+        }
+        const float inv = parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        unsigned char* to = rows_sm + (two ? 128 * w + row : row) * pitch;
+#pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t r[32];
-          tld32(tO + d, r);
-          tld_wait(r);
+          if (n > 0) {
+            tld32(tO + d, r);
+            tld_wait(r);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) jo[(d + e) * 128 + row] = __uint_as_float(r[e]);
+            for (int e = 0; e < 32; ++e) r[e] = 0;
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              y[e] = __uint_as_float(r[8 * c + e]);
+              if (join) y[e] = y[e] * f0 + jo[(d + 8 * c + e) * 128 + row] * f1;
+              y[e] *= inv;
+            }
+            if (parts > 1)
+              store8(reinterpret_cast<float*>(to) + d + 8 * c, y);
+            else
+              store8(reinterpret_cast<__nv_bfloat16*>(to) + d + 8 * c, y);
+          }
         }
-        jml[row] = make_float2(m, l);
+        if (live) {
+          if (parts > 1)
+            *part_ml(a, tile, split, pr - r0) = make_float2(m, l);
+          else if (a.lse)
+            a.lse[row_at(a, b, h, pr).lse] = lse_of(m, l);
+        }
       }
       streams_sync();
-    }
-    const bool join = !two && steps(1) > 0;
-    if (two || w == 0) {
-      float f0 = 1.f, f1 = 0.f;
-      if (join) {
-        const float2 ml = jml[row];
-        const float mn = fmaxf(m, ml.x);
-        f0 = fast_exp2(m - mn);
-        f1 = fast_exp2(ml.x - mn);
-        m = mn;
-        l = l * f0 + ml.y * f1;
+      // whole rows from there: a lane's own row to global memory would touch 32 lines
+      // a store (up to 8000 cycles a tile, 16 % of it)
+      if (parts > 1) {
+        constexpr int P = D / 4;
+        const int c = tid % P;
+        for (int r = tid / P; r < rt.r1 - r0; r += 256 / P)
+          *reinterpret_cast<uint4*>(part_o<D>(a, tile, split, r) + 4 * c) =
+              *reinterpret_cast<const uint4*>(rows_sm + r * pitch + 16 * c);
+      } else {
+        constexpr int P = D / 8;
+        const int c = tid % P;
+        for (int r = tid / P; r < rt.r1 - r0; r += 256 / P)
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + row_at(a, b, h, r0 + r).o + 8 * c) =
+              *reinterpret_cast<const uint4*>(rows_sm + r * pitch + 16 * c);
       }
-      if (sfail) l = m = __int_as_float(0x7FC00000);  // a wait gave up: no numbers, whoever reads the flag
-      const float inv = parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      unsigned char* to = rows_sm + (two ? 128 * w + row : row) * pitch;
-#pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
-        uint32_t r[32];
-        if (n > 0) {
-          tld32(tO + d, r);
-          tld_wait(r);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = 0;
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[e] = __uint_as_float(r[8 * c + e]);
-            if (join) y[e] = y[e] * f0 + jo[(d + 8 * c + e) * 128 + row] * f1;
-            y[e] *= inv;
-          }
-          if (parts > 1)
-            store8(reinterpret_cast<float*>(to) + d + 8 * c, y);
-          else
-            store8(reinterpret_cast<__nv_bfloat16*>(to) + d + 8 * c, y);
-        }
-      }
-      if (live) {
-        if (parts > 1)
-          *part_ml(a, tile, split, pr - r0) = make_float2(m, l);
-        else if (a.lse)
-          a.lse[row_at(a, b, h, pr).lse] = lse_of(m, l);
-      }
+      streams_sync();
+      if (sbad)
+        for (int r = r0 + warp; r < rt.r1; r += 8)
+          redo_row<__nv_bfloat16, CT, D>(a, s, b, h, r, t0, t1, tile, split, parts, r0);
     }
-    streams_sync();
-    // whole rows from there: a lane's own row to global memory would touch 32 lines
-    // a store (up to 8000 cycles a tile, 16 % of it)
-    if (parts > 1) {
-      constexpr int P = D / 4;
-      const int c = tid % P;
-      for (int r = tid / P; r < rt.r1 - r0; r += 256 / P)
-        *reinterpret_cast<uint4*>(part_o<D>(a, tile, split, r) + 4 * c) =
-            *reinterpret_cast<const uint4*>(rows_sm + r * pitch + 16 * c);
-    } else {
-      constexpr int P = D / 8;
-      const int c = tid % P;
-      for (int r = tid / P; r < rt.r1 - r0; r += 256 / P)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + row_at(a, b, h, r0 + r).o + 8 * c) =
-            *reinterpret_cast<const uint4*>(rows_sm + r * pitch + 16 * c);
-    }
-    streams_sync();
-    if (sbad)
-      for (int r = r0 + warp; r < rt.r1; r += 8)
-        redo_row<__nv_bfloat16, CT, D>(a, s, b, h, r, t0, t1, tile, split, parts, r0);
   }
   fence_before();
   __syncthreads();

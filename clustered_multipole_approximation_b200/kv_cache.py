@@ -64,6 +64,8 @@ def declare(lib) -> None:
     lib.muse_cache_read.argtypes = [vp, vp, sh, ca, ix, vp, vp, vp]
     lib.muse_attn_cache_workspace_size.restype = sz
     lib.muse_attn_cache_workspace_size.argtypes = [sh, ca, ix]
+    lib.muse_debug_inject_cache_fault.restype = None
+    lib.muse_debug_inject_cache_fault.argtypes = [i32]
     lib.muse_debug_cache_division.restype = i32
     lib.muse_debug_cache_division.argtypes = [sh, ca, ix, i32, i32, ctypes.POINTER(muse_cache_division)]
     lib.muse_attn_cache.restype = i32

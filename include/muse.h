@@ -486,6 +486,14 @@ int muse_profile_read(char *names, int name_stride, int *launches, double *ms,
  * thread-safe. */
 void muse_debug_inject_barrier_fault(int rank, int spin_limit);
 
+/* Failure-path testing.  While load >= 0, the chunk kernel of muse_attn_cache
+ * (bf16 queries, more than 32 packed rows of a kv-head) never reports the
+ * arrival of load number `load` of any CTA (loads: K and V tiles of 128 keys in
+ * the order K0 K1 V0 K2 V1 ...): the waits for it give up after half a second,
+ * the call records MUSE_DEVERR_MMA_WAIT and the rows are NaN.  load < 0 restores
+ * normal operation.  Not thread-safe. */
+void muse_debug_inject_cache_fault(int load);
+
 /* How muse_attn_cache divides its keys, for tests (host arithmetic; no pointer
  * is read): `tiles` row tiles of up to `rows` packed rows, `splits` CTAs each,
  * which join as a cluster or (splits > 1, cluster == 0) through the workspace;

@@ -7,7 +7,7 @@ import torch
 import clustered_multipole_approximation_b200 as muse
 from clustered_multipole_approximation_b200 import build
 from cache_ref import Paged, attend
-from test_gpu_cache import run_attend
+from test_gpu_cache import err_word, run_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,27 @@ def test_row_tiles_that_see_nothing_in_divided_calls(n, wide, B, Hkv, cache):
         P = Paged(B, Hkv, 64, kv, 16, cache, wide=wide)
         for causal in (True, False):
             run_attend(P, n, [n] * B, 4 * Hkv, causal=causal)
+
+
+@pytest.mark.parametrize("cache,D", [("bf16", 64), ("bf16", 128), ("e4m3", 64), ("i8", 128)])
+@pytest.mark.parametrize("n,wide,load", [(40, None, 0), (40, None, 15), (150, None, 6), (150, 400, 0), (40, 400, 3)])
+def test_a_load_that_never_arrives(n, wide, load, cache, D):
+    """Failure path of the chunk kernel: the waits for a load that is not reported
+    run out, the call says so and leaves NaN, unsplit and in splits; the next call
+    is as before."""
+    lib = muse.load_library()
+    P = Paged(1, 1, D, [900], 16, cache, wide=wide)
+    c, e = P.gpu(), err_word()
+    q = torch.randn(1, 1, n, D, generator=torch.Generator().manual_seed(8)).bfloat16().cuda()
+    want, _ = muse.muse_attn_cache(q, **c, lse=True)
+    lib.muse_debug_inject_cache_fault(load)
+    try:
+        o, lse = muse.muse_attn_cache(q, **c, lse=True, device_error=e)
+        with pytest.raises(muse.MuseError) as err:
+            muse.device_status(e)
+    finally:
+        lib.muse_debug_inject_cache_fault(-1)
+    assert err.value.status == 5 and int(e) == 1
+    assert o.isnan().all() and lse.isnan().all()
+    assert torch.equal(muse.muse_attn_cache(q, **c, device_error=e), want)
+    muse.device_status(e)
