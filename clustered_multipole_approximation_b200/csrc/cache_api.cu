@@ -28,9 +28,10 @@ muse_status check_launch() {
 }
 bool misaligned(const void* p, size_t a) { return p && (reinterpret_cast<uintptr_t>(p) % a) != 0; }
 
-muse_status check_shape(const muse_shape* sh) {
+// `queries`: the call has q-heads; else Hq may be 0, and its rows are not counted.
+muse_status check_shape(const muse_shape* sh, bool queries) {
   if (!sh) return fail(MUSE_ERR_INVALID_ARG, "shape must not be NULL");
-  if (sh->B < 1 || sh->Hq < 1 || sh->Hkv < 1 || sh->N < 1)
+  if (sh->B < 1 || sh->Hq < (queries ? 1 : 0) || sh->Hkv < 1 || sh->N < 1)
     return fail(MUSE_ERR_INVALID_ARG, "B, Hq, Hkv and N must be >= 1");
   if (sh->Hq % sh->Hkv) return fail(MUSE_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
   if (sh->D != 64 && sh->D != 128) return fail(MUSE_ERR_UNSUPPORTED, "D must be 64 or 128");
@@ -38,7 +39,7 @@ muse_status check_shape(const muse_shape* sh) {
     return fail(MUSE_ERR_INVALID_ARG, "dtype must be MUSE_BF16 or MUSE_F32");
   if (sh->out_f32) return fail(MUSE_ERR_UNSUPPORTED, "the cache calls answer in the input dtype (out_f32 = 0)");
   if (sh->N > 1 << 28) return fail(MUSE_ERR_UNSUPPORTED, "N must be <= 2^28");
-  const __int128 rows = (__int128)sh->B * sh->Hq * sh->N;
+  const __int128 rows = (__int128)sh->B * (queries ? sh->Hq : sh->Hkv) * sh->N;
   if (rows > (1LL << 31) - 1) return fail(MUSE_ERR_UNSUPPORTED, "B*H*N must be < 2^31");
   return MUSE_OK;
 }
@@ -133,7 +134,7 @@ extern "C" {
 muse_status muse_cache_write(const void* K, const muse_strides* ks, const void* V,
                              const muse_strides* vs, const muse_shape* sh, const muse_cache* ca,
                              const muse_cache_index* ix, int32_t* device_error, cudaStream_t st) {
-  muse_status s = check_shape(sh);
+  muse_status s = check_shape(sh, false);
   if (s == MUSE_OK) s = check_cache(ca, ix, sh->Hkv);
   if (s == MUSE_OK) s = check_strides(ks, sh);
   if (s == MUSE_OK) s = check_strides(vs, sh);
@@ -152,7 +153,7 @@ muse_status muse_cache_write(const void* K, const muse_strides* ks, const void* 
 muse_status muse_cache_read(void* K, void* V, const muse_shape* sh, const muse_cache* ca,
                             const muse_cache_index* ix, const int32_t* start,
                             int32_t* device_error, cudaStream_t st) {
-  muse_status s = check_shape(sh);
+  muse_status s = check_shape(sh, false);
   if (s == MUSE_OK) s = check_cache(ca, ix, sh->Hkv);
   if (s != MUSE_OK) return s;
   if (!K || !V) return fail(MUSE_ERR_INVALID_ARG, "K and V must not be NULL");
@@ -169,7 +170,7 @@ muse_status muse_cache_read(void* K, void* V, const muse_shape* sh, const muse_c
 
 size_t muse_attn_cache_workspace_size(const muse_shape* sh, const muse_cache* ca,
                                       const muse_cache_index* ix) {
-  if (check_shape(sh) != MUSE_OK || check_cache(ca, ix, sh->Hkv) != MUSE_OK) return 0;
+  if (check_shape(sh, true) != MUSE_OK || check_cache(ca, ix, sh->Hkv) != MUSE_OK) return 0;
   return cache_attn_workspace(attn_args(sh, ca, ix, nullptr));
 }
 
@@ -178,7 +179,7 @@ void muse_debug_inject_cache_fault(int load) { set_cache_fault(load < 0 ? -1 : l
 muse_status muse_debug_cache_division(const muse_shape* sh, const muse_cache* ca,
                                       const muse_cache_index* ix, int window, int len,
                                       muse_cache_division* out) {
-  muse_status s = check_shape(sh);
+  muse_status s = check_shape(sh, true);
   if (s == MUSE_OK) s = check_cache(ca, ix, sh->Hkv);
   if (s != MUSE_OK) return s;
   if (!out || window < 0 || len < 0 || len > ix->wide * ca->page_size)
@@ -198,7 +199,7 @@ muse_status muse_attn_cache(const void* Q, const muse_strides* qs, void* O, cons
                             float* lse, const muse_shape* sh, const muse_cache* ca,
                             const muse_cache_index* ix, float scale, int causal, int window,
                             int32_t* device_error, void* ws, size_t ws_bytes, cudaStream_t st) {
-  muse_status s = check_shape(sh);
+  muse_status s = check_shape(sh, true);
   if (s == MUSE_OK) s = check_cache(ca, ix, sh->Hkv);
   if (s == MUSE_OK) s = check_strides(qs, sh);
   if (s == MUSE_OK) s = check_strides(os, sh);

@@ -7,7 +7,7 @@ import pytest
 
 import clustered_multipole_approximation_b200 as muse
 from clustered_multipole_approximation_b200 import build
-from clustered_multipole_approximation_b200.kv_cache import muse_cache, muse_cache_division, muse_cache_index
+from clustered_multipole_approximation_b200.kv_cache import muse_cache, muse_cache_division, muse_cache_index, muse_strides
 
 FAKE = 0x1000  # never dereferenced
 
@@ -46,6 +46,22 @@ def test_every_length_has_its_splits(lib, dtype, cache, D):
             if d.splits > 1 and not d.cluster:  # partial rows, maxima and sums
                 assert size >= d.tiles * d.splits * d.rows * (D * 4 + 8), what
             assert not d.cluster or d.splits <= 8, what
+
+
+def test_writes_and_reads_need_no_query_heads(lib):
+    """Hq = 0, and a number of q-heads whose rows alone would be too many, pass the
+    shape's checks (an unknown cache dtype, checked later, is what is refused)."""
+    ca, ix = muse_cache(FAKE, FAKE, None, None, 4, 16, 9), muse_cache_index(FAKE, FAKE, None, 2)
+    st = muse_strides(384, 192, 64)
+    for Hq in (0, 2, 1 << 30):
+        sh = muse.muse_shape(2, Hq, 2, 3, 64, 0, 0)
+        assert lib.muse_cache_write(FAKE, st, FAKE, st, sh, ca, ix, None, None) == 1
+        assert b"cache dtype" in lib.muse_last_error()
+        assert lib.muse_cache_read(FAKE, FAKE, sh, ca, ix, None, None, None) == 1
+        assert b"cache dtype" in lib.muse_last_error()
+    sh = muse.muse_shape(2, 0, 2, 3, 64, 0, 0)
+    assert lib.muse_attn_cache(FAKE, st, FAKE, st, None, sh, ca, ix, 1.0, 1, 0, None, FAKE, 1 << 40, None) == 1
+    assert b"Hq" in lib.muse_last_error()
 
 
 def test_refusals(lib):
