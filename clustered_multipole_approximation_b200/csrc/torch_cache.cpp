@@ -9,10 +9,12 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/fill.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <optional>
 #include <string>
 
@@ -318,10 +320,17 @@ PyObject* attn_cache(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const Place p(a.dev, o[15]);
     p.uses_arguments(o, n);
 
+    // rows that are not there (i >= new_len) of an output made here: o = 0, lse = -inf
+    const bool ragged = o[5] != Py_None;
+    auto fill = [&](at::Tensor& t, double x) {
+      const c10::cuda::CUDAStreamGuard on_it(p.stream);
+      at::fill_(t, x);
+    };
     at::Tensor out, lse, ws;
     if (o[11] == Py_None) {
       out = at::empty(q.sizes(), q.options());
       p.uses(out);
+      if (ragged) fill(out, 0.);
     } else {
       out = tensor(o[11], "out");
       if (out.sizes() != q.sizes() || out.scalar_type() != q.scalar_type())
@@ -331,6 +340,7 @@ PyObject* attn_cache(PyObject*, PyObject* const* o, Py_ssize_t n) {
     if (o[12] == Py_True) {
       lse = at::empty({B, Hq, N}, q.options().dtype(at::kFloat));
       p.uses(lse);
+      if (ragged) fill(lse, -INFINITY);
     } else if (o[12] != Py_None) {
       lse = tensor(o[12], "lse");
       if (!has_shape(lse, {B, Hq, N}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous())

@@ -156,8 +156,9 @@ def muse_attn_cache(q, k_cache, v_cache, table, kv_len, *, new_len=None, scale=1
     the last `window` positions if it is not 0, or over all kv_len positions
     with causal=False (cross attention).  Returns o [B,Hq,n,D] in q's dtype
     or, with lse=True or an fp32 [B,Hq,n] tensor to write to, (o, lse).  Rows
-    i >= new_len of o and lse are left as they were.  out may not share memory
-    with q."""
+    i >= new_len of tensors that the caller gives are left as they were; of o
+    and lse made here they are 0 and -inf (a fill, some 2 us: calls that repeat
+    give out).  out may not share memory with q."""
     if stream is not None:
         stream = _stream(stream, k_cache.device)
     return (_bound or _native()).attn_cache(q, k_cache, v_cache, table, kv_len, new_len, scale, causal, window,

@@ -6,8 +6,8 @@ import torch
 
 import clustered_multipole_approximation_b200 as muse
 from clustered_multipole_approximation_b200 import build
-from cache_ref import Paged, attend
-from test_gpu_cache import err_word, run_attend
+from cache_ref import IN, Paged, attend
+from test_gpu_cache import err_word, i32, run_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +95,26 @@ def test_a_load_that_never_arrives(n, wide, load, cache, D):
     assert o.isnan().all() and lse.isnan().all()
     assert torch.equal(muse.muse_attn_cache(q, **c, device_error=e), want)
     muse.device_status(e)
+
+
+@pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("i8", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("n", [1, 4, 150])
+@pytest.mark.parametrize("other", [False, True])
+def test_rows_that_are_not_there_of_outputs_made_by_the_call(other, n, cache, dtype):
+    """o = 0 and lse = -inf behind new_len, whatever the memory held before."""
+    P = Paged(3, 1, 64, [300, n, 40], 16, cache)
+    c, new = P.gpu(), i32([n, n // 2, 0])
+    q = torch.randn(3, 2, n, 64, generator=torch.Generator().manual_seed(2)).to(IN[dtype]).cuda()
+    stream = torch.cuda.Stream() if other else None
+    seen = []
+    for _ in range(3):
+        junk = [torch.full((3, 2, n, 64), float("nan"), dtype=IN[dtype], device="cuda") for _ in range(4)]
+        junk += [torch.full((3, 2, n), float("nan"), device="cuda") for _ in range(4)]
+        del junk
+        o, lse = muse.muse_attn_cache(q, **c, new_len=new, lse=True, stream=stream)
+        torch.cuda.synchronize()
+        for b, m in enumerate([n, n // 2, 0]):
+            assert (o[b, :, m:] == 0).all() and (lse[b, :, m:] == -float("inf")).all()
+            assert o[b, :, :m].isfinite().all() and lse[b, :, :m].isfinite().all()
+        seen.append((o.clone(), lse.clone()))
+    assert all(torch.equal(a, b) for x in seen[1:] for a, b in zip(x, seen[0]))
