@@ -4,7 +4,9 @@
     python -m clustered_multipole_approximation_b200.build [--force] [--ptxas-v]
 
 Each .cu under csrc/ is compiled in parallel into _build/, then linked into
-clustered_multipole_approximation_b200/libmuse.so next to this file.
+clustered_multipole_approximation_b200/libmuse.so next to this file.  The module
+needs g++ and the headers of Python and torch; without them libmuse.so is built
+all the same, with a warning.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +26,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuse.so")
 TORCH_SRC = os.path.join(CSRC, "torch_cache.cpp")
 TORCH_LIB = os.path.join(PKG, "_torch_cache.so")
+TORCH_KEY = os.path.join(BUILD, "torch_cache.key")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -52,19 +56,37 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _cxx() -> str:
+    cxx = shutil.which("g++")
+    if cxx is None:
+        raise RuntimeError("g++ not found: it is needed to build _torch_cache.so")
+    return cxx
+
+
+def _torch_key() -> str:
+    """What a built module belongs to: this torch and this Python."""
+    import sysconfig
+
+    import torch
+    return "torch %s, %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+
+
 def build_torch(force: bool = False) -> str:
     """The CPython module; libmuse.so has to stand next to it."""
     header = os.path.join(INCLUDE, "muse.h")
-    if (not force and os.path.exists(TORCH_LIB)
+    key = _torch_key()
+    if (not force and os.path.exists(TORCH_LIB) and os.path.exists(TORCH_KEY)
             and all(os.path.getmtime(p) <= os.path.getmtime(TORCH_LIB) for p in (TORCH_SRC, header, __file__))):
-        return TORCH_LIB
+        with open(TORCH_KEY) as f:
+            if f.read() == key:
+                return TORCH_LIB
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     tmp = TORCH_LIB + ".tmp.%d" % os.getpid()
-    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+    cmd = [_cxx(), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE,
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
@@ -75,12 +97,27 @@ def build_torch(force: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"g++ failed on {TORCH_SRC}:\n{p.stderr}")
     os.replace(tmp, TORCH_LIB)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(TORCH_KEY, "w") as f:
+        f.write(key)
     return TORCH_LIB
+
+
+def _build_torch_or_warn(force: bool = False) -> None:
+    """Every call but the paged cache's does without the module: where it cannot
+    be compiled, libmuse.so stays usable, and a module of other sources goes."""
+    try:
+        build_torch(force)
+    except (RuntimeError, OSError, ImportError) as e:
+        if os.path.exists(TORCH_LIB):
+            os.remove(TORCH_LIB)
+        warnings.warn(f"_torch_cache.so was not built, the paged-cache calls will raise: {e}", RuntimeWarning,
+                      stacklevel=3)
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and up_to_date():
-        build_torch()
+        _build_torch_or_warn()
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -104,7 +141,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError("link failed:\n" + p.stderr)
     os.replace(tmp, LIB)
-    build_torch(force)
+    _build_torch_or_warn(force)
     return LIB
 
 
