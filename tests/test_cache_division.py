@@ -64,6 +64,30 @@ def test_writes_and_reads_need_no_query_heads(lib):
     assert b"Hq" in lib.muse_last_error()
 
 
+def test_buffers_that_share_memory_are_refused(lib):
+    """K and V of a read, and the caches and scales of a write, over the same memory
+    or a part of it."""
+    far = 1 << 40
+    sh, ix, st = muse.muse_shape(2, 2, 2, 3, 64, 0, 0), muse_cache_index(FAKE, FAKE, None, 2), muse_strides(384, 192, 64)
+    ca = muse_cache(FAKE, far, None, None, 4, 16, 0)
+    size = 2 * 2 * 3 * 64 * 2
+    for v in (FAKE, FAKE + size - 16, FAKE - size + 16):
+        assert lib.muse_cache_read(FAKE, v, sh, ca, ix, None, None, None) == 1
+        assert b"share" in lib.muse_last_error(), v
+    cells = 4 * 2 * 16
+    other = muse_strides(384, 64, 128)
+    for dt, bytes_ in ((0, 2), (1, 4)):
+        for v in (FAKE, FAKE + cells * 64 * bytes_ - 16):
+            for V, vs in ((far, st), (FAKE, other)) if v == FAKE else ((FAKE, st),):
+                ca = muse_cache(FAKE, v, None, None, 4, 16, dt)
+                assert lib.muse_cache_write(FAKE, st, V, vs, sh, ca, ix, None, None) == 1
+                assert b"share" in lib.muse_last_error()
+    for v, vs_ in ((FAKE + cells * 64 - 16, far), (far, FAKE), (far, FAKE + 4 * cells - 4)):
+        ca = muse_cache(FAKE, v, FAKE, vs_, 4, 16, 3)
+        assert lib.muse_cache_write(FAKE, st, far, st, sh, ca, ix, None, None) == 1
+        assert b"share" in lib.muse_last_error()
+
+
 def test_refusals(lib):
     sh, ca, ix = muse.muse_shape(1, 1, 1, 1, 64, 0, 0), muse_cache(FAKE, FAKE, None, None, 4, 16, 0), \
         muse_cache_index(FAKE, FAKE, None, 2)

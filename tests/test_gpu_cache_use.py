@@ -150,3 +150,24 @@ def test_e4m3_values_of_nan_under_fp32_queries(n):
         o = muse.muse_attn_cache(q.cuda(), **c, scale=D ** -0.5).double().cpu().numpy()
         assert (np.abs(o - ro) <= to)[:, :, ~sees].all()
         assert np.isnan(o[:, :, sees] if which == "k_cache" else o[:, :, sees, 5]).all()
+
+
+@pytest.mark.parametrize("cache", [torch.bfloat16, torch.int8])
+def test_one_cache_for_keys_that_are_values(cache):
+    """K and V of the same rows may live in one cache; read back into two tensors
+    beside one another."""
+    c = muse.make_cache(6, 2, 16, 64, cache)
+    for x in ("_cache", "_scale"):
+        if "k" + x in c:
+            c["v" + x] = c["k" + x]
+    args = dict(c, table=i32([[4, 0, 5]]), kv_len=i32([40]))
+    k = torch.randn(1, 2, 40, 64, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    muse.muse_cache_write(k, k, **args)
+    with pytest.raises(muse.MuseError, match="share"):
+        muse.muse_cache_write(k, k.clone(), **args)
+    out = torch.empty(2, 1, 2, 40, 64, dtype=torch.bfloat16, device="cuda")
+    rk, rv = muse.muse_cache_read(**args, N=40, out=(out[0], out[1]))
+    assert torch.equal(rk, rv) and rk.data_ptr() == out.data_ptr()
+    assert ((rk.float() - k.float()).abs() <= k.float().abs().amax(-1, keepdim=True) / 127 + 1e-2).all()
+    with pytest.raises(muse.MuseError, match="share"):
+        muse.muse_cache_read(**args, N=40, out=(out[0], out[0]))
