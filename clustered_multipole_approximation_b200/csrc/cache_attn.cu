@@ -138,8 +138,9 @@ Path plan_keys(CacheAttn& a, long long cap) {
   a.cluster = 0;
   a.quantum = p == kWide ? 64 : kQuantum;
   if (p == kWide) {
-    // in blocks of 64 keys: two CTAs an SM at a time, half a wave lost at the end,
-    // 0.3 of a block for a split's start and partials
+    // in blocks of 64 keys: two CTAs an SM at a time (at D = 128 the kernel has one,
+    // and the same division), half a wave lost at the end, 0.3 of a block for a split's
+    // start and partials
     double best = 1e30;
     for (int S = 1; S <= 64 && (S == 1 || (long long)S * 64 < cap + 64); ++S) {
       if (S > 1 && units * S > 0x7FFFFFFF) break;
