@@ -26,7 +26,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuse.so")
 TORCH_SRC = os.path.join(CSRC, "torch_cache.cpp")
 TORCH_LIB = os.path.join(PKG, "_torch_cache.so")
-TORCH_KEY = os.path.join(BUILD, "torch_cache.key")
+TORCH_KEY = TORCH_LIB + ".key"  # travels with the module
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -71,15 +71,25 @@ def _torch_key() -> str:
     return "torch %s, %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
 
 
+def _torch_built_for():
+    """The key of the module that is there; None where nothing says so."""
+    if not os.path.exists(TORCH_KEY):
+        return None
+    with open(TORCH_KEY) as f:
+        return f.read()
+
+
+def _torch_stale() -> bool:
+    """Whether the module is older than its sources."""
+    t = os.path.getmtime(TORCH_LIB)
+    return any(os.path.getmtime(p) > t for p in (TORCH_SRC, os.path.join(INCLUDE, "muse.h"), __file__))
+
+
 def build_torch(force: bool = False) -> str:
     """The CPython module; libmuse.so has to stand next to it."""
-    header = os.path.join(INCLUDE, "muse.h")
     key = _torch_key()
-    if (not force and os.path.exists(TORCH_LIB) and os.path.exists(TORCH_KEY)
-            and all(os.path.getmtime(p) <= os.path.getmtime(TORCH_LIB) for p in (TORCH_SRC, header, __file__))):
-        with open(TORCH_KEY) as f:
-            if f.read() == key:
-                return TORCH_LIB
+    if not force and os.path.exists(TORCH_LIB) and not _torch_stale() and _torch_built_for() == key:
+        return TORCH_LIB
     import sysconfig
 
     import torch
@@ -97,7 +107,6 @@ def build_torch(force: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"g++ failed on {TORCH_SRC}:\n{p.stderr}")
     os.replace(tmp, TORCH_LIB)
-    os.makedirs(BUILD, exist_ok=True)
     with open(TORCH_KEY, "w") as f:
         f.write(key)
     return TORCH_LIB
@@ -105,11 +114,18 @@ def build_torch(force: bool = False) -> str:
 
 def _build_torch_or_warn(force: bool = False) -> None:
     """Every call but the paged cache's does without the module: where it cannot
-    be compiled, libmuse.so stays usable, and a module of other sources goes."""
+    be compiled, libmuse.so stays usable.  A module of other sources or of another
+    torch goes; one that nothing is known against stays."""
     try:
         build_torch(force)
     except (RuntimeError, OSError, ImportError) as e:
         if os.path.exists(TORCH_LIB):
+            try:
+                other = _torch_stale() or _torch_built_for() not in (None, _torch_key())
+            except ImportError:
+                other = True
+            if not other:
+                return
             os.remove(TORCH_LIB)
         warnings.warn(f"_torch_cache.so was not built, the paged-cache calls will raise: {e}", RuntimeWarning,
                       stacklevel=3)

@@ -11,7 +11,7 @@ from clustered_multipole_approximation_b200 import build
 def module(tmp_path, monkeypatch):
     """build() with a module of its own, up to date; the list of compilers' commands."""
     build.build()
-    lib, key = tmp_path / "_torch_cache.so", tmp_path / "torch_cache.key"
+    lib, key = tmp_path / "_torch_cache.so", tmp_path / "_torch_cache.so.key"
     lib.write_text("a module")
     key.write_text(build._torch_key())
     monkeypatch.setattr(build, "TORCH_LIB", str(lib))
@@ -60,3 +60,18 @@ def test_the_library_does_not_need_the_module(module, monkeypatch, why):
     assert os.path.exists(build.LIB) and not lib.exists()
     with pytest.raises((RuntimeError, ImportError)):
         build.build_torch()
+
+
+@pytest.mark.parametrize("change", ["no key", "older than its sources"])
+def test_a_shipped_module_stays_unless_it_is_of_other_sources(module, monkeypatch, change):
+    """A module that came without its key, on a box without a compiler."""
+    lib, key, _ = module
+    monkeypatch.setattr(build.shutil, "which", lambda x: None)
+    if change == "no key":
+        os.remove(key)
+        assert build.build() == build.LIB and lib.exists()
+    else:
+        os.utime(lib, (1, 1))
+        with pytest.warns(RuntimeWarning, match="paged-cache calls will raise"):
+            build.build()
+        assert not lib.exists()
