@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       if (!all_ok()) break;
       look(tile_at(w, k));
       __syncwarp();
-      if (lane < 2) mbar_arrive(smem_u32(&mP[w][lane]));
+      if (lane < 2 && ok) mbar_arrive(smem_u32(&mP[w][lane]));
     }
     for (int k = 0; !idle && k < n && all_ok(); ++k) {
       const int T = tile_at(w, k), tb = t0 + T * kKeys;
