@@ -91,8 +91,10 @@ bool overlaps(const muse_strides* s, const muse_shape* sh, int H) {
   return false;
 }
 
-// Whether two buffers of this size share memory.
-bool share(const void* a, const void* b, __int128 bytes) {
+// Whether two written buffers of this size share memory, other than one buffer
+// that gets the same twice.
+bool clash(const void* a, const void* b, __int128 bytes, bool same) {
+  if (a == b && same) return false;
   const __int128 x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + bytes && y < x + bytes;
 }
@@ -150,12 +152,11 @@ muse_status muse_cache_write(const void* K, const muse_strides* ks, const void* 
     return fail(MUSE_ERR_INVALID_ARG, "K and V must be 16-byte aligned");
   if (misaligned(device_error, 4))
     return fail(MUSE_ERR_INVALID_ARG, "device_error must be 4-byte aligned");
-  // one buffer for K and V holds both only where they are the same rows
   const int size = ca->dtype == MUSE_CACHE_BF16 ? 2 : ca->dtype == MUSE_CACHE_F32 ? 4 : 1;
-  const bool same = K == V && ca->k == ca->v && ks->b == vs->b && ks->h == vs->h && ks->t == vs->t;
+  const bool same = K == V && ks->b == vs->b && ks->h == vs->h && ks->t == vs->t;
   const __int128 rows = (__int128)ca->pages * sh->Hkv * ca->page_size;
-  if (!same && (share(ca->k, ca->v, rows * sh->D * size) ||
-                (size == 1 && share(ca->k_scale, ca->v_scale, rows * 4))))
+  if (clash(ca->k, ca->v, rows * sh->D * size, same) ||
+      (size == 1 && clash(ca->k_scale, ca->v_scale, rows * 4, same)))
     return fail(MUSE_ERR_INVALID_ARG, "the caches of K and V must not share memory");
   clear_error(device_error, st);
   run_cache_write(device_cache(sh, ca, ix, device_error), (int)ca->dtype, K, V, as_strides(ks),
@@ -174,7 +175,8 @@ muse_status muse_cache_read(void* K, void* V, const muse_shape* sh, const muse_c
     return fail(MUSE_ERR_INVALID_ARG, "K and V must be 16-byte aligned");
   if (misaligned(device_error, 4) || misaligned(start, 4))
     return fail(MUSE_ERR_INVALID_ARG, "start and device_error must be 4-byte aligned");
-  if (share(K, V, (__int128)sh->B * sh->Hkv * sh->N * sh->D * (sh->dtype == MUSE_F32 ? 4 : 2)))
+  if (clash(K, V, (__int128)sh->B * sh->Hkv * sh->N * sh->D * (sh->dtype == MUSE_F32 ? 4 : 2),
+            ca->k == ca->v && ca->k_scale == ca->v_scale))
     return fail(MUSE_ERR_INVALID_ARG, "K and V must not share memory");
   clear_error(device_error, st);
   Cache c = device_cache(sh, ca, ix, device_error);

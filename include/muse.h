@@ -419,8 +419,8 @@ typedef struct {
  * positions (new_len[b] > kv_len[b]) are not written.  No two new tokens may
  * share a cache row (a page named twice where new tokens go): what such a row
  * holds afterwards is undefined.  The caches of K and V share no memory (but one
- * cache may serve both where K and V are the same rows).  shape->Hq is not used (0 will do; if it is not
- * 0 it must be a multiple of Hkv).
+ * cache may serve both where K and V are the same rows).  shape->Hq is not used:
+ * 0 will do, and what is not 0 must be a multiple of Hkv.
  * device_error: one int32 or NULL; set to 0, then to MUSE_DEVERR_* bits.
  */
 muse_status muse_cache_write(const void *K, const muse_strides *ks, const void *V,
@@ -432,7 +432,7 @@ muse_status muse_cache_write(const void *K, const muse_strides *ks, const void *
  * Reads rows back: K and V [B,Hkv,N,D] (contiguous, shape->dtype, the layout
  * of the whole-sequence operators) receive positions start[b] .. start[b] +
  * N - 1 of every sequence (start NULL: 0), zero rows at and past kv_len[b].
- * They share no memory.
+ * They share no memory (but may be one tensor where the cache is one for both).
  * index->new_len is not used, nor is shape->Hq (0, or a multiple of Hkv).
  */
 muse_status muse_cache_read(void *K, void *V, const muse_shape *shape, const muse_cache *cache,

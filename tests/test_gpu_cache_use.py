@@ -169,5 +169,12 @@ def test_one_cache_for_keys_that_are_values(cache):
     rk, rv = muse.muse_cache_read(**args, N=40, out=(out[0], out[1]))
     assert torch.equal(rk, rv) and rk.data_ptr() == out.data_ptr()
     assert ((rk.float() - k.float()).abs() <= k.float().abs().amax(-1, keepdim=True) / 127 + 1e-2).all()
+    one = muse.muse_cache_read(**args, N=40, out=(out[1], out[1]))[0]
+    assert torch.equal(one, rk)
+    args["v_cache"] = args["v_cache"].clone()
     with pytest.raises(muse.MuseError, match="share"):
         muse.muse_cache_read(**args, N=40, out=(out[0], out[0]))
+    with pytest.raises(muse.MuseError, match="share"):
+        flat = out.flatten()
+        half = flat[:flat.numel() // 2].view_as(out[0]), flat[64:64 + flat.numel() // 2].view_as(out[0])
+        muse.muse_cache_read(**args, N=40, out=half)
